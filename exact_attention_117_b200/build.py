@@ -20,7 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libfa_b200.so")
 DEBUG_LIB = os.path.join(PKG, "libfa_b200_debug.so")
 SOURCES = ["fa_api.cu"]
-HEADERS = ["sm100.cuh", "common.cuh", "fwd.cuh", "bwd.cuh", "bwd_main.cuh", "dq_pass.cuh", "kv_outer.cuh"]
+HEADERS = ["sm100.cuh", "common.cuh", "fwd.cuh", "bwd.cuh", "bwd_main.cuh", "dq_pass.cuh", "kv_outer.cuh",
+           "rotary.cuh", "kv4.cuh", "kv4_attend.cuh", "kv4_host.cuh"]
 
 
 def nvcc() -> str:

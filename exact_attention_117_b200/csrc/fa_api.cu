@@ -580,7 +580,7 @@ fa_status fa_check_device_error(void* stream, unsigned int* detail) {
   if (word && cudaMemcpyToSymbol(fa::g_error_word, &zero, sizeof(zero)) != cudaSuccess)
     return FA_ERR_CUDA;
   if (detail) *detail = word;
-  return word ? FA_ERR_DEVICE_TIMEOUT : FA_OK;
+  return word == fa::kErrBadPage ? FA_ERR_PAGE : word ? FA_ERR_DEVICE_TIMEOUT : FA_OK;
 }
 
 fa_status fa_selftest_watchdog(unsigned int limit_ms, void* stream) {
@@ -602,6 +602,7 @@ const char* fa_status_string(fa_status s) {
     case FA_ERR_CUDA: return "CUDA runtime error";
     case FA_ERR_DEVICE_TIMEOUT: return "a kernel gave up on a bounded wait";
     case FA_ERR_STATE: return "timing calls out of order";
+    case FA_ERR_PAGE: return "a block table names a page outside the cache";
   }
   return "unknown status";
 }
@@ -646,6 +647,8 @@ fa_status fa_timing_end(float* ms_per_kernel, int* launches_per_kernel) {
   return st;
 }
 
-int fa_version(void) { return 100; }
+int fa_version(void) { return 200; }
 
 }  // extern "C"
+
+#include "kv4_host.cuh"

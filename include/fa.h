@@ -73,7 +73,8 @@ typedef enum {
   FA_ERR_WORKSPACE = 6,       /* workspace NULL or smaller than required         */
   FA_ERR_CUDA = 7,            /* a CUDA runtime call or launch failed            */
   FA_ERR_DEVICE_TIMEOUT = 8,  /* a kernel gave up on a bounded wait              */
-  FA_ERR_STATE = 9            /* timing calls out of order                       */
+  FA_ERR_STATE = 9,           /* timing calls out of order                       */
+  FA_ERR_PAGE = 10            /* a block table names a page outside the cache    */
 } fa_status;
 
 /*
@@ -232,10 +233,131 @@ FA_API fa_status fa_fwd_kv_outer(const void* q, const void* k, const void* v, vo
                                  float scale, void* workspace, size_t workspace_bytes,
                                  void* stream);
 
+/* Element types of the calls below that take one. */
+typedef enum { FA_BF16 = 0, FA_FP16 = 1, FA_FP32 = 2 } fa_dtype;
+
+/*
+ * Rotary positions.  The channels (x1, x2) of pair i of a head at position p
+ * become
+ *     y1 = A (x1 cos t - x2 sin t),  y2 = A (x2 cos t + x1 sin t),
+ * t = p * inv_freq[i]; channels from rotary_dim on pass through.
+ *   q, q_out : [B, q_heads, N, d];  k, k_out : [B, k_heads, N, d] (k_heads = 0:
+ *              no second tensor).  An output may be its input.
+ *   strides  : 12 element strides (batch, head, position) of q, q_out, k,
+ *              k_out; the last axis is contiguous.
+ *   positions: int32, or int64 if positions_64: entry b * position_stride + n
+ *              (a stride of 0 shares [N] positions).  Negative ones turn back.
+ *   inv_freq : rotary_dim / 2 radians per position, on the device.  Angles are
+ *              reduced in 64 bits, so far positions keep their phase.
+ *   interleaved : 0 pairs (i, i + rotary_dim / 2), else pairs (2i, 2i + 1).
+ *   amplitude : A.  inverse != 0 turns by -t: with the same A this is the
+ *              gradient of the call (dq_out, dk_out in, dq, dk out).
+ *   dtype    : FA_BF16, FA_FP16 or FA_FP32; products in 32 bits, one rounding.
+ * N = 0 does nothing.  FA_ERR_SHAPE for an odd rotary_dim or one above d,
+ * FA_ERR_ALIGN where an element (a pair, if interleaved) is not aligned to
+ * its size.
+ */
+FA_API fa_status fa_rotary(const void* q, const void* k, void* q_out, void* k_out, int B,
+                           int q_heads, int k_heads, int N, int d, const long long* strides,
+                           const void* positions, int positions_64, long long position_stride,
+                           const double* inv_freq, int rotary_dim, int interleaved,
+                           float amplitude, int inverse, int dtype, void* stream);
+
+/*
+ * The 4-bit key/value cache: uint8 [pages, kv_heads, page_size / 16, 18 d]
+ * (fa_kv4_cache_size bytes, 16-byte aligned; page_size a multiple of 16).  A
+ * tile of 18 d bytes holds 16 tokens of one kv head: K codes (16 rows of d/2
+ * bytes), K parameters (16 rows of d/64 pairs), V codes, V parameters.  The 64
+ * channels of a group share a pair of bf16 (scale, lowest); code n stands for
+ * lowest + scale * n.  32-bit word w of a row holds channels 8w .. 8w+7, the
+ * first in the lowest bits; word 4j + t of a K row stands at place t * d/32 + j,
+ * word 8j + g of a V row at place g * d/64 + j.
+ * A slot is page * page_size + place in the page.
+ */
+FA_API size_t fa_kv4_cache_size(int pages, int kv_heads, int page_size, int d);
+
+/*
+ * Pages and slots of a step, on the device.  Request b goes from lengths[b]
+ * cached tokens to new_lengths[b]:
+ *   - pages it needs more are popped from the ring of free pages, in request
+ *     order, and entered into its row of block_table; pages it no longer
+ *     needs (a shorter length, 0 to end a request) are pushed onto the ring
+ *     and are free from the next call on;
+ *   - its new tokens (new - old, if positive) take positions old .. new - 1;
+ *     packed over the requests, positions[t] and slots[t] describe token t and
+ *     cu_tokens[b] .. cu_tokens[b + 1] request b's range.  From the last token
+ *     to max_tokens: slot -1, position 0.
+ * The ring: free_pages[i mod ring_size], head <= i < tail, with free_range =
+ * {head, tail} (both only grow; ring_size at least the number of pages).
+ * lengths_out and free_range_out may be lengths and free_range themselves.
+ * *status: 0, or a sum of 1 (too few free pages), 2 (more than max_tokens new
+ * tokens), 4 (a length below 0 or above width * page_size), 8 (an impossible
+ * ring); if it is not 0 nothing is changed: lengths and range come out as they
+ * went in, and every slot is -1.
+ * Entries of a row past its pages are left as they are, and never read.
+ */
+FA_API fa_status fa_kv4_plan(const int* lengths, const int* new_lengths, int* block_table,
+                             long long table_stride, int width, int* free_pages, int ring_size,
+                             const long long* free_range, int requests, int page_size,
+                             int max_tokens, int* lengths_out, long long* free_range_out,
+                             int* cu_tokens, long long* slots, int* positions, int* status,
+                             void* stream);
+
+/*
+ * Keys and values into the cache.  k, v: bf16 [tokens, kv_heads, d], strides =
+ * element strides (token, head) of k, then of v, multiples of 8.  Per token,
+ * head and group of 64 channels: lowest = min x, scale = the smallest bf16 with
+ * 15 scale >= max x - min x, n = floor((x - lowest) / scale + 1/2) (0 where
+ * scale is 0); comparisons are exact.  A group with an infinity, a NaN or a
+ * span beyond the largest float reads back as NaN.  Slots outside the cache
+ * (-1) are skipped; the slots of a call must differ.
+ *
+ * fa_kv4_gather reads slots back as bf16 [tokens, kv_heads, d] (strides of k,
+ * then of v): lowest + scale * n, rounded to 32 bits and to bf16; zeros for
+ * slots outside the cache.
+ */
+FA_API fa_status fa_kv4_append(const void* k, const void* v, void* cache, const long long* slots,
+                               long long tokens, int kv_heads, int d, int pages, int page_size,
+                               const long long* strides, void* stream);
+FA_API fa_status fa_kv4_gather(const void* cache, const long long* slots, void* k, void* v,
+                               long long tokens, int kv_heads, int d, int pages, int page_size,
+                               const long long* strides, void* stream);
+
+/*
+ * Attention of packed queries over the 4-bit cache.
+ *   q, o   : bf16 or fp16 (dtype) [tokens, heads, d]; strides = element strides
+ *            (token, head) of q, then of o, multiples of 8.
+ *   lse    : fp32 [tokens, heads].
+ *   cu_tokens[b] .. cu_tokens[b + 1] are request b's query rows; they are its
+ *            newest tokens.  lengths[b] counts its cached keys, the queries'
+ *            own among them.
+ *   block_table : int32 [requests, width], row stride table_stride.
+ *   causal : query i of n sees keys 0 .. lengths[b] - n + i; else all of them.
+ *            A row that sees no key gets O = 0, LSE = -infinity.
+ * heads is a multiple of kv_heads; head h reads kv head h / (heads / kv_heads).
+ * max_tokens: an upper bound on a request's query rows as the caller knows it;
+ * it only chooses the kernel and sizes the workspace (larger requests are
+ * still right).  Rows of q past cu_tokens[requests] are not touched.
+ * Deterministic: the same arguments give the same bits.
+ *   workspace : fa_kv4_attention_workspace_size bytes, 16-byte aligned,
+ *               contents on entry irrelevant.
+ * A page index outside the cache is reported as FA_ERR_PAGE by
+ * fa_check_device_error; its keys count as absent.
+ */
+FA_API size_t fa_kv4_attention_workspace_size(int heads, int kv_heads, int d, int max_tokens);
+FA_API fa_status fa_kv4_attention(const void* q, const void* cache, const int* block_table,
+                                  const int* lengths, const int* cu_tokens, void* o, float* lse,
+                                  int requests, int tokens, int heads, int kv_heads, int d,
+                                  int pages, int page_size, int width, long long table_stride,
+                                  const long long* strides, int max_tokens, int causal,
+                                  float scale, int dtype, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
 /*
  * Synchronises `stream`, then reads and clears the device error word of the
  * current device.  Returns FA_OK, FA_ERR_DEVICE_TIMEOUT (a bounded wait ran
- * out; *detail, if non-NULL, receives which one) or FA_ERR_CUDA.
+ * out; *detail, if non-NULL, receives which one), FA_ERR_PAGE (only page
+ * indices outside a cache were met) or FA_ERR_CUDA.
  */
 FA_API fa_status fa_check_device_error(void* stream, unsigned int* detail);
 
@@ -263,7 +385,13 @@ typedef enum {
                               dQ pass (fa_bwd_deterministic)         */
   FA_KERNEL_FWD_COMBINE = 4, /* split-KV forward: merge of the splits */
   FA_KERNEL_FWD_KV_OUTER = 5, /* forward in the KV-outer loop order    */
-  FA_KERNEL_COUNT = 6
+  FA_KERNEL_ROTARY = 6,      /* rotary positions                       */
+  FA_KERNEL_KV4_PLAN = 7,    /* pages and slots of the 4-bit cache     */
+  FA_KERNEL_KV4_APPEND = 8,  /* keys and values into the 4-bit cache   */
+  FA_KERNEL_KV4_GATHER = 9,  /* values of slots of the 4-bit cache     */
+  FA_KERNEL_KV4_ATTEND = 10, /* attention over the 4-bit cache         */
+  FA_KERNEL_KV4_COMBINE = 11, /* its merge of partial results          */
+  FA_KERNEL_COUNT = 12
 } fa_kernel_id;
 
 /*
