@@ -28,6 +28,7 @@ enum : unsigned int {
   kErrAlign = 1u << 14,      // dynamic shared memory base not 1 KiB aligned
   kErrSelfTest = 1u << 15,   // the watchdog self-test kernel gave up (as it must)
   kErrBadPage = 1u << 16,    // a page index of a block table lies outside the cache
+  kErrKv4 = 1u << 4,         // attention over the 4-bit cache
   kErrDebugCheck = 1u << 17, // a bounds check of the FA_DEBUG build failed (see dbg_check)
 };
 

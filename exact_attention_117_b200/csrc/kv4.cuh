@@ -41,6 +41,20 @@ struct Kv4Tile {
   }
 };
 
+// Division of 0 <= n < 2^31 by a divisor known at launch: one high product, an
+// addition and a shift (m = floor(2^32 (2^s - d) / d) + 1, 2^s >= d).
+struct FastDiv {
+  uint32_t mul, shift, by;
+  static FastDiv of(uint32_t d) {
+    uint32_t s = 0;
+    while ((1ull << s) < d) ++s;
+    return {static_cast<uint32_t>((((1ull << s) - d) << 32) / d + 1), s, d};
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
+    return (__umulhi(n, mul) + n) >> shift;
+  }
+};
+
 struct Kv4StoreParams {
   const __nv_bfloat16* x[2];  // keys, values
   __nv_bfloat16* y[2];        // of a gather

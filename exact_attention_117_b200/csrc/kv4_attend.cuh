@@ -3,17 +3,18 @@
 //   O_i = sum_j softmax_j(scale q_i . K_j) V_j over the keys row i sees,
 //   LSE_i = ln sum_j exp(scale q_i . K_j),
 // where K_j and V_j are the values the cache's codes stand for.  With K_j =
-// mid + s (n - 8) per group of 64 channels (mid = lowest + 8 s),
-//   q . K_j = sum_groups s (q . (n - 8)) + mid (sum of q),
-// so the matrix instructions multiply the codes themselves and scale and mid
-// act on the 64-channel sums; for V, P s goes into the matrix instructions and
-// P mid is summed beside them.
+// lowest + s n per group of 64 channels,
+//   q . K_j = sum_groups s (q . n) + lowest (sum of q),
+// so the matrix instructions multiply the codes themselves, and scale and
+// lowest act on the 64-channel sums; for V, P s goes into the matrix
+// instructions and P lowest is summed beside them.
 //
-// Codes are small whole numbers, exact in fp16.  q enters as fp16 after an
-// exact scaling of each row by a power of two (largest element in [1, 2)), so
-// a bf16 q keeps all its bits down to 2^-24 of the row's largest.  P s enters
-// as fp16 relative to a power of two above the largest s seen: 11 bits,
-// against the 8 of a bf16 P.  Scores, softmax statistics and O are fp32.
+// Codes enter as fp16 subnormal numbers, exactly.  q enters as fp16 after an
+// exact scaling of each row by a power of two (its largest element near fp16's
+// largest), so a bf16 or fp16 q keeps all its bits down to 2^-24 of the row's
+// largest.  P s enters as fp16 relative to a power of two above the largest s
+// seen: 11 bits, against the 8 of a bf16 P.  Scores, softmax statistics and O
+// are fp32.
 //
 // Rows: the queries of a request times the heads that share a kv head, in
 // tiles of 8 NT.  Transposed products (S^T = K q^T, O^T = V^T P^T) put tokens
@@ -42,22 +43,24 @@ struct Kv4AttendParams {
   long long q_st, q_sh, o_st, o_sh;  // strides in elements
   long long table_stride;
   int requests, heads, kv_heads, group, tokens, pages, page_size, width;
+  FastDiv page_tiles, by_group;  // 16-key tiles of a page, heads of a group
   float scale_log2;
   int causal, is_half;
+  uint64_t limit_ns;      // of a bounded wait
 };
 
 constexpr int kKv4Warps = 4;
-constexpr int kKv4Chunk = 16 * kKv4Warps;  // keys of a work unit
+constexpr int kKv4Chunk = 32 * kKv4Warps;  // keys of a work unit
 
 // ------------------------------------------------------------ the work's order
-// Units: (request, row tile, kv head, chunk of keys), chunks innermost.  CTA c
-// of n takes units [c U / n, (c + 1) U / n): every CTA reads the same share of
-// the cache whatever the lengths are.  A (request, row tile, head) that a
+// Units: (request, row tile, kv head, chunk of keys), chunks innermost.  Each CTA
+// takes an equal, contiguous range of them, and so reads the same share of the
+// cache whatever the lengths are.  A (request, row tile, head) that a
 // CTA's range cuts is left as partial results, which the combine kernel joins.
 struct Kv4Req {
   int first, n, len, row_tiles, chunks;
 };
-template <int ROWS>
+template <int ROWS>  // rows of a tile
 __device__ __forceinline__ Kv4Req kv4_request(const Kv4AttendParams& p, int b) {
   Kv4Req r;
   r.first = min(max(p.cu_tokens[b], 0), p.tokens);
@@ -72,63 +75,76 @@ __device__ __forceinline__ long long kv4_units(const Kv4AttendParams& p, const K
   return static_cast<long long>(r.row_tiles) * p.kv_heads * r.chunks;
 }
 
+// a / b for non-negative numbers, in 32 bits where they fit (nearly always).
+__device__ __forceinline__ long long kv4_div(long long a, long long b) {
+  if (((a | b) >> 32) == 0)
+    return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+struct Kv4Share {  // of the units: CTA c of n starts at each * c + min(c, rest)
+  long long each;
+  int rest;
+  __device__ __forceinline__ Kv4Share(long long total, int n) {
+    each = kv4_div(total, n);
+    rest = static_cast<int>(total - each * n);
+  }
+  __device__ __forceinline__ long long start(int c) const { return each * c + min(c, rest); }
+};
+
 struct Kv4Shared {
   long long warp_sum[kKv4Warps];
   long long total, found_excl;
   int found_b;
 };
 
-// Block-wide: the total number of units, and the request that holds unit
-// share_of(total) together with the units before it (-1 if there is none).
-template <int ROWS, typename F>
-__device__ __forceinline__ void kv4_locate(const Kv4AttendParams& p, Kv4Shared& sh, F share_of) {
+// Block-wide: the total number of units, and the request that holds the first
+// unit of CTA `cta` of `ctas` together with the units before it (-1 if there is
+// none).  Up to 128 requests are summed once, more are walked twice.
+template <int ROWS>
+__device__ __forceinline__ void kv4_locate(const Kv4AttendParams& p, Kv4Shared& sh, int cta,
+                                           int ctas) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kThreads = kKv4Warps * 32;
   const int chunks = (p.requests + kThreads - 1) / kThreads;
-  long long total = 0;
+  long long total = 0, mine = 0, incl = 0;
+  if (tid == 0) sh.found_b = -1;
   for (int pass = 0; pass < 2; ++pass) {
     long long base = 0;
     for (int c = 0; c < chunks; ++c) {
       const int b = c * kThreads + tid;
-      const long long mine = b < p.requests ? kv4_units(p, kv4_request<ROWS>(p, b)) : 0;
-      long long incl = mine;
+      if (pass == 0 || chunks > 1) {
+        mine = b < p.requests ? kv4_units(p, kv4_request<ROWS>(p, b)) : 0;
+        incl = mine;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
-      }
-      __syncthreads();
-      if (lane == 31) sh.warp_sum[warp] = incl;
-      __syncthreads();
-      long long all = 0;
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += x;
+        }
+        __syncthreads();
+        if (lane == 31) sh.warp_sum[warp] = incl;
+        __syncthreads();
+        long long all = 0;
 #pragma unroll
-      for (int w = 0; w < kKv4Warps; ++w) {
-        if (w < warp) incl += sh.warp_sum[w];
-        all += sh.warp_sum[w];
+        for (int w = 0; w < kKv4Warps; ++w) {
+          if (w < warp) incl += sh.warp_sum[w];
+          all += sh.warp_sum[w];
+        }
+        if (pass == 0) total += all;
+        else incl += base;
+        base += all;
       }
       if (pass == 1) {
-        const long long u = share_of(total), e = base + incl - mine;
-        if (u >= e && u < e + mine) {
+        const long long u = Kv4Share(total, ctas).start(cta);
+        if (u >= incl - mine && u < incl) {
           sh.found_b = b;
-          sh.found_excl = e;
+          sh.found_excl = incl - mine;
         }
-      }
-      base += all;
-    }
-    if (pass == 0) {
-      total = base;
-      if (tid == 0) {
-        sh.total = total;
-        sh.found_b = -1;
       }
     }
   }
+  if (tid == 0) sh.total = total;
   __syncthreads();
-}
-
-// Range start of CTA c of n.
-__device__ __forceinline__ long long kv4_start(long long total, int c, int n) {
-  return total / n * c + total % n * c / n;
 }
 
 // ------------------------------------------------------------ matrix pieces
@@ -151,21 +167,18 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-// Codes 0..7 of a word as four fp16 pairs n - 8: (0, 4), (1, 5), (2, 6), (3, 7).
-// A code under the bits of 1024.0 reads 1024 + n, one four bits higher 1024 +
-// 16 n; one addition or fused multiply-add takes the offset off, exactly.
+// Codes 0..7 of a word as four fp16 pairs: (0, 4), (1, 5), (2, 6), (3, 7).  Four
+// bits at the bottom of an fp16 are the subnormal number n 2^-24, four bits
+// higher 16 n 2^-24: exact operands of the matrix instructions without any
+// conversion (adding 1024 under the bits and taking it off again costs another
+// instruction a pair).  The factor 16 is taken out of q beforehand and of O
+// afterwards, 2^24 out of the scores' factor and of O.
 __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&h)[4]) {
   const uint32_t w8 = w >> 8;
-  uint32_t a, b, c, d;
-  asm("lop3.b32 %0, %1, 0x000f000f, 0x64006400, 0xea;" : "=r"(a) : "r"(w));
-  asm("lop3.b32 %0, %1, 0x00f000f0, 0x64006400, 0xea;" : "=r"(b) : "r"(w));
-  asm("lop3.b32 %0, %1, 0x000f000f, 0x64006400, 0xea;" : "=r"(c) : "r"(w8));
-  asm("lop3.b32 %0, %1, 0x00f000f0, 0x64006400, 0xea;" : "=r"(d) : "r"(w8));
-  const uint32_t off1 = 0xe408e408u, sixteenth = 0x2c002c00u, off16 = 0xd480d480u;  // -1032, 1/16, -72
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(h[0]) : "r"(a), "r"(off1));
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(h[1]) : "r"(b), "r"(sixteenth), "r"(off16));
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(h[2]) : "r"(c), "r"(off1));
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(h[3]) : "r"(d), "r"(sixteenth), "r"(off16));
+  h[0] = w & 0x000f000fu;
+  h[1] = w & 0x00f000f0u;
+  h[2] = w8 & 0x000f000fu;
+  h[3] = w8 & 0x00f000f0u;
 }
 
 template <int W>
@@ -188,316 +201,532 @@ __device__ __forceinline__ int kv4_tau(int r) { return (r >> 1) + 4 * (r & 1); }
 template <int D, int NT>
 struct Kv4AttendLayout {
   static constexpr int kRows = 8 * NT;
+  static constexpr int kFast = NT <= 2 ? 2 : 1;  // tiles taken together where all rows see them
+  static constexpr int kCtas = NT == 1 ? 3 : 2;  // resident on an SM, by registers
+  static constexpr int kBlock = 2 * Kv4Tile<D>::kBytes;  // 32 keys: one stage
+  static constexpr int kStages = D == 64 && NT == 1 ? 5 : 4;
+  static constexpr int kRing = kKv4Warps * kStages * kBlock;
   static constexpr int kPitch = D + 4;  // floats of a row in the merge buffer
+  // the merge buffer lies over the ring, which is empty by then
   static constexpr int kOffMl = kKv4Warps * kRows * kPitch * 4;
-  static constexpr int kBytes = kOffMl + 2 * kKv4Warps * kRows * 4;
+  static constexpr int kMerge = kOffMl + 2 * kKv4Warps * kRows * 4;
+  static constexpr int kOffQ = kRing > kMerge ? kRing : kMerge;
+  // more than two row tiles share their q fragments through shared memory
+  static constexpr int kOffQs = kOffQ + (NT > 2 ? NT * (D / 32) * 32 * 16 : 0);
+  static constexpr int kOffRs = kOffQs + (NT > 2 ? NT * (D / 64) * 8 * 4 : 0);  // sums of q, factors
+  static constexpr int kOffBar = kOffRs + (NT > 2 ? kRows * 4 : 0);
+  static constexpr int kBytes = kOffBar + kKv4Warps * kStages * 8;
   static constexpr int kPartFloats = kRows * (D + 2);  // O, then m and l
+  static_assert(kOffBar % 8 == 0 && kCtas * (kBytes + 256 + 1024) <= 233472, "shared memory");
 };
 
-// One partial or final result from the per-warp results in shared memory.
-template <int D, int NT>
-__device__ __forceinline__ void kv4_store_row(const Kv4AttendParams& p, const Kv4Req& rq, int h,
-                                              int row, int ch, float o, float m, float l) {
-  // `row` of the request: query row / group, head h group + row % group
-  const int tok = rq.first + row / p.group, head = h * p.group + row % p.group;
-  const float out = l == 0.f ? 0.f : o / l;
-  const long long at = tok * p.o_st + head * p.o_sh + ch;
-  if (p.is_half)
-    static_cast<__half*>(p.o)[at] = __float2half_rn(out);
+template <int N>
+__device__ __forceinline__ void load_floats(const float* at, float (&v)[N]) {
+  if (N == 4) {
+    const float4 x = *reinterpret_cast<const float4*>(at);
+    v[0] = x.x, v[1] = x.y, v[2 % N] = x.z, v[3 % N] = x.w;
+  } else {
+    const float2 x = *reinterpret_cast<const float2*>(at);
+    v[0] = x.x, v[1] = x.y;
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_floats(float* at, const float (&v)[N]) {
+  if (N == 4)
+    *reinterpret_cast<float4*>(at) = make_float4(v[0], v[1], v[2 % N], v[3 % N]);
   else
-    static_cast<__nv_bfloat16*>(p.o)[at] = __float2bfloat16_rn(out);
-  if (ch == 0)
+    *reinterpret_cast<float2*>(at) = make_float2(v[0], v[1]);
+}
+
+// A finished row of a request (query row / group, head h group + row % group)
+// by a whole warp, lane's channels D / 32 lane and on; o is not yet over l.
+template <int D>
+__device__ __forceinline__ void kv4_store_row(const Kv4AttendParams& p, const Kv4Req& rq, int h,
+                                              int row, int lane, const float (&o)[D / 32], float m,
+                                              float l) {
+  const int i = p.by_group(row), tok = rq.first + i, head = h * p.group + row - i * p.group;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const long long at = tok * p.o_st + head * p.o_sh + lane * (D / 32);
+  uint32_t w[D / 64];
+#pragma unroll
+  for (int k = 0; k < D / 64; ++k)
+    w[k] = p.is_half ? pack_f16x2(o[2 * k] * inv, o[2 * k + 1] * inv)
+                     : pack_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv);
+  uint16_t* to = static_cast<uint16_t*>(p.o) + at;
+  if (D == 128)
+    *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[D / 64 - 1]);
+  else
+    *reinterpret_cast<uint32_t*>(to) = w[0];
+  if (lane == 0)
     p.lse[static_cast<long long>(tok) * p.heads + head] =
         l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
+// Row r of a tile (of `rows` real ones) for the lane's fragments: q as fp16
+// times a power of two that brings the row's largest element to [2^14, 2^15)
+// (the power itself kept within 2^+-100), every other channel pair a sixteenth
+// of that; the sums of q over the groups beside scores in units of 2^-24; the
+// factor from those scores to base-2 exponents.
+template <int D>
+__device__ __forceinline__ void kv4_rows(const Kv4AttendParams& p, const Kv4Req& rq, int h,
+                                         int row0, int r, int rows, uint32_t (&f)[D / 32][4],
+                                         float (&sum)[D / 64], float& factor) {
+  const int t = threadIdx.x & 3;
+  float x[D / 32][8], top = 0.f;
+  const int i = p.by_group(row0 + r);
+  const long long at = (rq.first + i) * p.q_st + (h * p.group + row0 + r - i * p.group) * p.q_sh;
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) {
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    if (r < rows)
+      raw = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at + 32 * j + 8 * t);
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (p.is_half) {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+        x[j][2 * k] = v.x;
+        x[j][2 * k + 1] = v.y;
+      } else {
+        x[j][2 * k] = bf16_lo(w[k]);
+        x[j][2 * k + 1] = bf16_hi(w[k]);
+      }
+      top = fmaxf(top, fmaxf(fabsf(x[j][2 * k]), fabsf(x[j][2 * k + 1])));
+    }
+  }
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23), 27), 227);
+  const float down = __uint_as_float(static_cast<uint32_t>(254 + 14 - e) << 23);
+#pragma unroll
+  for (int gp = 0; gp < D / 64; ++gp) sum[gp] = 0.f;
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float less = k & 1 ? down * 0.0625f : down;
+      f[j][k] = pack_f16x2(x[j][k] * less, x[j][k + 4] * less);
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f[j][k]));
+      sum[j / 2] = fmaf(v.x + v.y, k & 1 ? 16.f : 1.f, sum[j / 2]);
+    }
+#pragma unroll
+  for (int gp = 0; gp < D / 64; ++gp) {
+    sum[gp] += __shfl_xor_sync(0xffffffffu, sum[gp], 1);
+    sum[gp] += __shfl_xor_sync(0xffffffffu, sum[gp], 2);
+    sum[gp] *= 0x1p-24f;
+  }
+  factor = __uint_as_float(static_cast<uint32_t>(e + 10) << 23) * p.scale_log2;
+}
+
+// Running state of a warp's rows (columns 2t, 2t + 1 of each row tile).
 template <int D, int NT>
-__global__ void __launch_bounds__(kKv4Warps * 32)
+struct Kv4State {
+  float acc[D / 64][4][NT][4];  // O^T 2^-24 vinv, odd channels times 16
+  float lo_sum[NT][D / 64][2];  // sum of P times V's lowest values
+  float l[NT][2], m[NT][2];
+  float vinv;                   // a power of two: the largest scale of V times it is below 8
+};
+
+// A lane's places in a tile: K code words of its two rows' first, their
+// parameters, V code words of its four tokens' first.
+template <int D>
+struct Kv4Lane {
+  uint32_t k, par, v;
+  __device__ __forceinline__ Kv4Lane() {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, tau = kv4_tau(g);
+    k = tau * Kv4Tile<D>::kRow + t * (D / 32) * 4;
+    par = tau * Kv4Tile<D>::kPar;
+    v = t * Kv4Tile<D>::kRow + g * (D / 64) * 4;
+  }
+};
+
+// kTiles tiles of 16 adjacent keys from shared memory.  kMasked: some row does
+// not see all of them (keys no row sees may hold anything).
+template <int D, int NT, int kTiles, bool kMasked>
+__device__ __forceinline__ void kv4_tiles(const uint8_t* tile, const Kv4Lane<D>& at,
+                                          const uint8_t* q_smem,
+                                          const uint32_t (&qf)[NT > 2 ? 1 : NT][D / 32][4],
+                                          const float (&qs)[NT][D / 64][2],
+                                          const float (&rs)[NT][2], const int (&lim)[NT][2],
+                                          int key0, int any_sees, Kv4State<D, NT>& st) {
+  using T = Kv4Tile<D>;
+  constexpr int kGroups = D / 64, kKW = D / 32, kVW = D / 64, kTok = 2 * kTiles;
+  const int lane = threadIdx.x & 31;
+  // the lane's tokens in the score fragments: tau and tau + 8 of each tile
+  uint32_t kp[kTok][kGroups], vp[kTok][kGroups];
+  float s[kTiles][NT][kGroups][4] = {};
+  // ---- S^T = K q^T, by groups
+#pragma unroll
+  for (int u = 0; u < kTiles; ++u) {
+    const uint8_t* base = tile + u * T::kBytes;
+    uint32_t k0[kKW], k1[kKW];
+    load_words<kKW>(base + at.k, k0);
+    load_words<kKW>(base + at.k + 8 * T::kRow, k1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      load_words<kGroups>(base + at.par + T::kOffKPar + 8 * i * T::kPar, kp[2 * u + i]);
+      load_words<kGroups>(base + at.par + T::kOffVPar + 8 * i * T::kPar, vp[2 * u + i]);
+    }
+#pragma unroll
+    for (int j = 0; j < kKW; ++j) {
+      uint32_t a[4], c[4];
+      codes_f16(k0[j], a);
+      codes_f16(k1[j], c);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        uint4 f;
+        if (NT > 2)
+          f = *reinterpret_cast<const uint4*>(q_smem + ((nt * kKW + j) * 32 + lane) * 16);
+        else
+          f = make_uint4(qf[nt % (NT > 2 ? 1 : NT)][j][0], qf[nt % (NT > 2 ? 1 : NT)][j][1],
+                         qf[nt % (NT > 2 ? 1 : NT)][j][2], qf[nt % (NT > 2 ? 1 : NT)][j][3]);
+        mma_f16(s[u][nt][j / 2], a[0], c[0], a[1], c[1], f.x, f.y);
+        mma_f16(s[u][nt][j / 2], a[2], c[2], a[3], c[3], f.z, f.w);
+      }
+    }
+  }
+  int key[kTok];
+  float vs[kTok][kGroups], vl[kTok][kGroups], x[NT][2 * kTok], y[NT][2 * kTok];
+  float most = 0.f;
+#pragma unroll
+  for (int i = 0; i < kTok; ++i) {
+    key[i] = key0 + kv4_tau(lane >> 2) + 8 * i;
+    const bool gone = kMasked && key[i] >= any_sees;
+#pragma unroll
+    for (int gp = 0; gp < kGroups; ++gp) {
+      vs[i][gp] = gone ? 0.f : bf16_lo(vp[i][gp]) * st.vinv;
+      vl[i][gp] = gone ? 0.f : bf16_hi(vp[i][gp]);
+    }
+    most = kGroups == 2 ? fmax3(vs[i][0], vs[i][kGroups - 1], most) : fmaxf(vs[i][0], most);
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int c = 0; c < 2 * kTok; ++c) {
+      const int i = c >> 1, r = c & 1;
+      float v = 0.f;
+#pragma unroll
+      for (int gp = 0; gp < kGroups; ++gp)
+        v = fmaf(bf16_lo(kp[i][gp]), s[i >> 1][nt][gp][c & 3], fmaf(bf16_hi(kp[i][gp]), qs[nt][gp][r], v));
+      x[nt][c] = v;
+      y[nt][c] = fmaf(v, rs[nt][r], -st.m[nt][r]);
+      if (kMasked && key[i] >= lim[nt][r]) y[nt][c] = -INFINITY;
+    }
+#pragma unroll
+    for (int c = 0; c < 2 * kTok; c += 2) most = fmax3(y[nt][c], y[nt][c + 1], most);
+  }
+  // ---- the running reference moves only when a score passes it by 2^8 (or a
+  // scale of V passes its own): P stays below 2^8, far from fp16's largest, and
+  // most tiles need no reduction over lanes
+  if (__any_sync(0xffffffffu, most > 8.f)) {
+    float top = 0.f, vf = 1.f;
+#pragma unroll
+    for (int i = 0; i < kTok; ++i)
+#pragma unroll
+      for (int gp = 0; gp < kGroups; ++gp)
+        if (!kMasked || key[i] < any_sees) top = fmaxf(top, bf16_lo(vp[i][gp]));
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (st.vinv == 0.f || top * st.vinv > 8.f) {  // the largest to [4, 8)
+      const uint32_t e = min(max(__float_as_uint(top) >> 23, 2u), 254u);
+      const float next = __uint_as_float((256u - e) << 23);
+      vf = st.vinv == 0.f ? 0.f : next / st.vinv;
+      st.vinv = next;
+#pragma unroll
+      for (int i = 0; i < kTok; ++i)
+#pragma unroll
+        for (int gp = 0; gp < kGroups; ++gp)
+          vs[i][gp] = kMasked && key[i] >= any_sees ? 0.f : bf16_lo(vp[i][gp]) * next;
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float hi = -INFINITY;
+#pragma unroll
+        for (int c = r; c < 2 * kTok; c += 2)
+          if (!kMasked || key[c >> 1] < lim[nt][r]) hi = fmaxf(hi, x[nt][c] * rs[nt][r]);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        float f = 1.f;
+        if (hi > st.m[nt][r]) {
+          f = ex2_approx(st.m[nt][r] - hi);
+          st.m[nt][r] = hi;
+        }
+        st.l[nt][r] *= f;
+#pragma unroll
+        for (int gp = 0; gp < kGroups; ++gp) st.lo_sum[nt][gp][r] *= f;
+#pragma unroll
+        for (int j = 0; j < kVW; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            st.acc[j][i][nt][r] *= f * vf;
+            st.acc[j][i][nt][r + 2] *= f * vf;
+          }
+#pragma unroll
+        for (int c = r; c < 2 * kTok; c += 2) {
+          y[nt][c] = fmaf(x[nt][c], rs[nt][r], -st.m[nt][r]);
+          if (kMasked && key[c >> 1] >= lim[nt][r]) y[nt][c] = -INFINITY;
+        }
+      }
+  }
+  // ---- P, P s as B fragments, P lowest
+  uint32_t pb[kTiles][NT][kGroups][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float e[2 * kTok];
+#pragma unroll
+    for (int c = 0; c < 2 * kTok; ++c) {
+      e[c] = ex2_approx(y[nt][c]);
+      st.l[nt][c & 1] += e[c];
+    }
+#pragma unroll
+    for (int gp = 0; gp < kGroups; ++gp)
+#pragma unroll
+      for (int i = 0; i < kTok; ++i) {
+        float pv[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const bool hidden = kMasked && key[i] >= lim[nt][r];
+          pv[r] = hidden ? 0.f : e[2 * i + r] * vs[i][gp];
+          st.lo_sum[nt][gp][r] = hidden ? st.lo_sum[nt][gp][r]
+                                        : fmaf(e[2 * i + r], vl[i][gp], st.lo_sum[nt][gp][r]);
+        }
+        pb[i >> 1][nt][gp][i & 1] = transpose8(pack_f16x2(pv[0], pv[1]));
+      }
+  }
+  // ---- O^T += V^T P^T
+#pragma unroll
+  for (int u = 0; u < kTiles; ++u) {
+    uint32_t vw[4][kVW];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      load_words<kVW>(tile + u * T::kBytes + at.v + T::kOffV + 4 * i * T::kRow, vw[i]);
+#pragma unroll
+    for (int j = 0; j < kVW; ++j)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t sel = half ? 0x7632u : 0x5410u;
+        uint32_t a[4], c[4];
+        codes_f16(__byte_perm(vw[0][j], vw[1][j], sel), a);
+        codes_f16(__byte_perm(vw[2][j], vw[3][j], sel), c);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint32_t b0 = pb[u][nt][j][0], b1 = pb[u][nt][j][1];
+          mma_f16(st.acc[j][2 * half][nt], a[0], a[1], c[0], c[1], b0, b1);
+          mma_f16(st.acc[j][2 * half + 1][nt], a[2], a[3], c[2], c[3], b0, b1);
+        }
+      }
+  }
+}
+
+// The bounded wait, with everything but its first look out of line.
+__device__ __noinline__ bool kv4_wait_long(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                           volatile int* abort_flag) {
+  return wait_bounded_warp(bar, parity, limit_ns, abort_flag, kErrKv4 | kErrRoleLoad);
+}
+__device__ __forceinline__ bool kv4_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                         volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
+         kv4_wait_long(bar, parity, limit_ns, abort_flag);
+}
+
+// Each warp walks its own blocks of 32 keys (every fourth of the CTA's) through
+// its own ring of stages, filled by bulk copies of whole tiles: no barrier
+// between warps until their results are joined.
+template <int D, int NT>
+__global__ void __launch_bounds__(kKv4Warps * 32, (Kv4AttendLayout<D, NT>::kCtas))
     kv4_attend_kernel(const __grid_constant__ Kv4AttendParams p) {
   using T = Kv4Tile<D>;
   using L = Kv4AttendLayout<D, NT>;
-  constexpr int kGroups = D / 64, kKW = D / 32, kVW = D / 64;
-  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int kGroups = D / 64, kKW = D / 32, kVW = D / 64, kS = L::kStages;
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Kv4Shared sh;
+  __shared__ int abort_word;
+  volatile int* abort_flag = &abort_word;
   float* merge = reinterpret_cast<float*>(smem);
   float* s_m = reinterpret_cast<float*>(smem + L::kOffMl);
   float* s_l = s_m + kKv4Warps * L::kRows;
+  float* s_qs = reinterpret_cast<float*>(smem + L::kOffQs);
+  float* s_rs = reinterpret_cast<float*>(smem + L::kOffRs);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
+  constexpr int kFast = L::kFast;
+  const Kv4Lane<D> places;
   const int ctas = gridDim.x, cta = blockIdx.x;
-  kv4_locate<L::kRows>(p, sh, [&](long long total) { return kv4_start(total, cta, ctas); });
-  const long long u_begin = kv4_start(sh.total, cta, ctas), u_end = kv4_start(sh.total, cta + 1, ctas);
+  const uint8_t* ring = smem + warp * kS * L::kBlock;
+  const uint32_t ring_at = smem_u32(ring);
+  const uint32_t bars = smem_u32(smem + L::kOffBar) + warp * kS * 8;
+  if (lane == 0)
+    for (int i = 0; i < kS; ++i) mbar_init(bars + 8 * i, 1);
+  if (tid == 0) abort_word = 0;
+  fence_barrier_init();
+  fence_proxy_async_smem();
+  kv4_locate<L::kRows>(p, sh, cta, ctas);
+  const Kv4Share share(sh.total, ctas);
+  const long long u_begin = share.start(cta), u_end = share.start(cta + 1);
   if (u_begin >= u_end) return;
   int b = sh.found_b;
   long long excl = sh.found_excl;
   Kv4Req rq = kv4_request<L::kRows>(p, b);
+  const int tiles_per_page = p.page_size / 16;
+  int it = 0;  // blocks this warp has taken from its ring
 
   for (long long u = u_begin; u < u_end;) {
     while (u - excl >= kv4_units(p, rq)) {
       excl += kv4_units(p, rq);
       rq = kv4_request<L::kRows>(p, ++b);
     }
-    const long long job = (u - excl) / rq.chunks;
+    const long long job = kv4_div(u - excl, rq.chunks);
     const int c0 = static_cast<int>(u - excl - job * rq.chunks);
     const int c1 = static_cast<int>(min(static_cast<long long>(rq.chunks), c0 + (u_end - u)));
-    const int h = static_cast<int>(job % p.kv_heads);
-    const int row0 = static_cast<int>(job / p.kv_heads) * L::kRows;
+    const int tile_row = static_cast<int>(kv4_div(job, p.kv_heads));
+    const int h = static_cast<int>(job - static_cast<long long>(tile_row) * p.kv_heads);
+    const int row0 = tile_row * L::kRows;
     const int rows = min(L::kRows, rq.n * p.group - row0);
+    // keys that query token i of the request sees
+    auto sees = [&](int i) {
+      return p.causal ? min(max(rq.len - rq.n + i + 1, 0), rq.len) : rq.len;
+    };
+    const int all_see = sees(p.by_group(row0)), any_sees = sees(p.by_group(row0 + rows - 1));
 
-    // ---- the rows: q as B fragments, sums over groups, factor, visible keys
-    uint32_t qf[NT][kKW][4];
+    // ---- fill the ring; pages of the block after next are looked up an
+    // iteration ahead of their copy
+    const int tile_end = min(c1 * (kKv4Chunk / 16), (any_sees + 15) / 16);
+    const int blk0 = c0 * kKv4Warps + warp;
+    const int n_blk = max(0, ((tile_end + 1) / 2 - blk0 + kKv4Warps - 1) / kKv4Warps);
+    const int* table = p.table + b * p.table_stride;
+    const uint8_t* head_base = p.cache + static_cast<long long>(h) * tiles_per_page * T::kBytes;
+    const long long page_bytes = static_cast<long long>(p.kv_heads) * tiles_per_page * T::kBytes;
+    // Lane 0 looks up and copies a block's first tile, lane 1 its second; both
+    // are a block ahead with the look-up.
+    uint32_t present = 0;  // two bits a stage: its tiles are there
+    int tile = 2 * blk0 + lane, fill = it % kS;
+    long long from = -1;  // the lane's next tile in the cache, -1: none
+    auto look_up = [&]() {
+      from = -1;
+      if (lane < 2 && tile < tile_end) {
+        const int page = p.page_tiles(tile), id = table[page];
+        if (static_cast<unsigned>(id) < static_cast<unsigned>(p.pages))
+          from = id * page_bytes + (tile - page * tiles_per_page) * T::kBytes;
+        else
+          atomicOr(&g_error_word, kErrBadPage);
+      }
+      tile += 2 * kKv4Warps;
+    };
+    auto copy = [&]() {  // (a block past the end: nothing is expected)
+      const uint32_t two = __ballot_sync(0xffffffffu, from >= 0);
+      present = (present & ~(3u << (2 * fill))) | two << (2 * fill);
+      const uint32_t bar = bars + 8 * fill;
+      if (lane < 2) {
+        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(two) * T::kBytes);
+        if (from >= 0)
+          bulk_load(ring_at + fill * L::kBlock + lane * T::kBytes, head_base + from, T::kBytes, bar);
+      }
+      if (++fill == kS) fill = 0;
+    };
+    const int n_fill = min(kS - 1, n_blk);
+    for (int i = 0; i < n_fill; ++i) {
+      look_up();
+      copy();
+    }
+    look_up();
+
+    // ---- the rows: q as B fragments, its sums over groups, factors
+    uint32_t qf[NT > 2 ? 1 : NT][kKW][4];
     float qs[NT][kGroups][2], rs[NT][2];
     int lim[NT][2];
-    int all_see = 0x7fffffff, any_sees = 0;
+    if (NT > 2) {  // warp nt lays out row tile nt for all
+      if (warp < NT) {
+        float sum[kGroups], factor;
+        kv4_rows<D>(p, rq, h, row0, 8 * warp + g, rows, qf[0], sum, factor);
+#pragma unroll
+        for (int j = 0; j < kKW; ++j)
+          *reinterpret_cast<uint4*>(smem + L::kOffQ + ((warp * kKW + j) * 32 + lane) * 16) =
+              make_uint4(qf[0][j][0], qf[0][j][1], qf[0][j][2], qf[0][j][3]);
+        if (t == 0) {
+#pragma unroll
+          for (int gp = 0; gp < kGroups; ++gp) s_qs[(warp * kGroups + gp) * 8 + g] = sum[gp];
+          s_rs[8 * warp + g] = factor;
+        }
+      }
+      __syncthreads();
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = 8 * nt + g;  // this lane's row of the B fragments
-      float x[kKW][8], top = 0.f;
-      const bool real = r < rows;
-      const int row = row0 + r;
-      const long long at = real ? (rq.first + row / p.group) * p.q_st +
-                                      (h * p.group + row % p.group) * p.q_sh
-                                : 0;
-#pragma unroll
-      for (int j = 0; j < kKW; ++j) {
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (real)
-          raw = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at + 32 * j + 8 * t);
-        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (p.is_half) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-            x[j][2 * i] = f.x;
-            x[j][2 * i + 1] = f.y;
-          } else {
-            x[j][2 * i] = bf16_lo(w[i]);
-            x[j][2 * i + 1] = bf16_hi(w[i]);
-          }
-          top = fmaxf(top, fmaxf(fabsf(x[j][2 * i]), fabsf(x[j][2 * i + 1])));
-        }
-      }
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // 2^e with top / 2^e in [1, 2); kept within 2^+-100
-      const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23), 27), 227);
-      const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-      const float up = __uint_as_float(static_cast<uint32_t>(e) << 23);
-      float sum[kGroups] = {};
-#pragma unroll
-      for (int j = 0; j < kKW; ++j) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          qf[nt][j][i] = pack_f16x2(x[j][i] * down, x[j][i + 4] * down);
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&qf[nt][j][i]));
-          sum[j / 2] += f.x + f.y;
-        }
-      }
-#pragma unroll
-      for (int gp = 0; gp < kGroups; ++gp) {
-        sum[gp] += __shfl_xor_sync(0xffffffffu, sum[gp], 1);
-        sum[gp] += __shfl_xor_sync(0xffffffffu, sum[gp], 2);
-      }
-      // from the lane of a row (g = row) to the lanes of its column (t)
+      float sum[kGroups], factor = 0.f;
+      if (NT <= 2)
+        kv4_rows<D>(p, rq, h, row0, 8 * nt + g, rows, qf[nt % (NT > 2 ? 1 : NT)], sum, factor);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int src = (2 * t + i) * 4;
+        const int r = 8 * nt + 2 * t + i;
+        // from a lane of the row (g = row) to the lanes of its column (t)
 #pragma unroll
         for (int gp = 0; gp < kGroups; ++gp)
-          qs[nt][gp][i] = __shfl_sync(0xffffffffu, sum[gp], src);
-        rs[nt][i] = __shfl_sync(0xffffffffu, up, src) * p.scale_log2;
-        const int rr = 8 * nt + 2 * t + i;
-        int see = rq.len;
-        if (p.causal) see = min(max(rq.len - rq.n + (row0 + rr) / p.group + 1, 0), rq.len);
-        lim[nt][i] = rr < rows ? see : 0;
-        if (rr < rows) {
-          all_see = min(all_see, see);
-          any_sees = max(any_sees, see);
-        }
+          qs[nt][gp][i] = NT > 2 ? s_qs[(nt * kGroups + gp) * 8 + 2 * t + i]
+                                 : __shfl_sync(0xffffffffu, sum[gp], (2 * t + i) * 4);
+        rs[nt][i] = NT > 2 ? s_rs[r] : __shfl_sync(0xffffffffu, factor, (2 * t + i) * 4);
+        lim[nt][i] = r < rows ? sees(p.by_group(row0 + r)) : 0;
       }
     }
-    all_see = __reduce_min_sync(0xffffffffu, all_see);
-    any_sees = __reduce_max_sync(0xffffffffu, any_sees);
 
-    float acc[kVW][4][NT][4] = {};
-    float lo_sum[NT][kGroups][2] = {}, l[NT][2] = {}, m[NT][2], thr[NT][2];
-    float vref = 0.f, vinv = 0.f;
+    Kv4State<D, NT> st = {};
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        m[nt][i] = 0.f;
-        thr[nt][i] = -INFINITY;
-      }
+    for (int nt = 0; nt < NT; ++nt) st.m[nt][0] = st.m[nt][1] = -3.402823466e38f;  // below every score
 
-    const int kt_end = min(c1 * kKv4Warps, (any_sees + 15) / 16);
-    for (int kt = c0 * kKv4Warps + warp; kt < kt_end; kt += kKv4Warps) {
-      const int key0 = kt * 16;
-      const int page = p.table[b * p.table_stride + key0 / p.page_size];
-      if (page < 0 || page >= p.pages) {  // reported, and read as absent keys
-        if (lane == 0) atomicOr(&g_error_word, kErrBadPage);
-        continue;
+    bool ok = true;
+    int i = 0, stage = it % kS, key0 = 32 * blk0;
+    uint32_t parity = (it / kS) & 1;
+    for (; i < n_blk; ++i) {
+      if (i + kS - 1 < n_blk) {
+        copy();
+        look_up();
       }
-      const uint8_t* tile =
-          p.cache + ((static_cast<long long>(page) * p.kv_heads + h) * (p.page_size / 16) +
-                     key0 % p.page_size / 16) * T::kBytes;
-      uint32_t k0[kKW], k1[kKW], kp0[kGroups], kp1[kGroups], vp0[kGroups], vp1[kGroups], vw[4][kVW];
-      const int tau = kv4_tau(g);
-      load_words<kKW>(tile + tau * T::kRow + t * kKW * 4, k0);
-      load_words<kKW>(tile + (tau + 8) * T::kRow + t * kKW * 4, k1);
-      load_words<kGroups>(tile + T::kOffKPar + tau * T::kPar, kp0);
-      load_words<kGroups>(tile + T::kOffKPar + (tau + 8) * T::kPar, kp1);
-      load_words<kGroups>(tile + T::kOffVPar + tau * T::kPar, vp0);
-      load_words<kGroups>(tile + T::kOffVPar + (tau + 8) * T::kPar, vp1);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        load_words<kVW>(tile + T::kOffV + (t + 4 * i) * T::kRow + g * kVW * 4, vw[i]);
-
-      // ---- S^T = K q^T, by groups
-      float s[NT][kGroups][4] = {};
-#pragma unroll
-      for (int j = 0; j < kKW; ++j) {
-        uint32_t a[4], c[4];
-        codes_f16(k0[j], a);
-        codes_f16(k1[j], c);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_f16(s[nt][j / 2], a[0], c[0], a[1], c[1], qf[nt][j][0], qf[nt][j][1]);
-          mma_f16(s[nt][j / 2], a[2], c[2], a[3], c[3], qf[nt][j][2], qf[nt][j][3]);
-        }
+      if (!kv4_wait(bars + 8 * stage, parity, p.limit_ns, abort_flag)) {
+        ok = false;
+        break;
       }
-      const bool masked = key0 + 16 > all_see;
-      const int key[2] = {key0 + tau, key0 + tau + 8};
-      float ks[2][kGroups], km[2][kGroups], vs[2][kGroups], vm[2][kGroups];
-      bool again = false;
-#pragma unroll
-      for (int gp = 0; gp < kGroups; ++gp) {
-        ks[0][gp] = bf16_lo(kp0[gp]);
-        ks[1][gp] = bf16_lo(kp1[gp]);
-        km[0][gp] = fmaf(8.f, ks[0][gp], bf16_hi(kp0[gp]));
-        km[1][gp] = fmaf(8.f, ks[1][gp], bf16_hi(kp1[gp]));
-        vs[0][gp] = bf16_lo(vp0[gp]);
-        vs[1][gp] = bf16_lo(vp1[gp]);
-        vm[0][gp] = fmaf(8.f, vs[0][gp], bf16_hi(vp0[gp]));
-        vm[1][gp] = fmaf(8.f, vs[1][gp], bf16_hi(vp1[gp]));
-        // keys no row sees may hold anything
-        if (masked) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (key[i] >= any_sees) vs[i][gp] = vm[i][gp] = 0.f;
-        }
-        again |= vs[0][gp] > vref || vs[1][gp] > vref;
-      }
-      float x[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int i = c >> 1, r = c & 1;
-          float v = 0.f;
-#pragma unroll
-          for (int gp = 0; gp < kGroups; ++gp)
-            v += ks[i][gp] * s[nt][gp][c] + km[i][gp] * qs[nt][gp][r];
-          v *= rs[nt][r];
-          if (masked && key[i] >= lim[nt][r]) v = -INFINITY;
-          x[nt][c] = v;
-          again |= v > thr[nt][r];
-        }
-      // ---- the running reference moves only when a score passes it by 2^8
-      // (or a scale of V passes its own): P stays below 2^8, far from fp16's
-      // largest, and most tiles need no reduction over lanes
-      if (__any_sync(0xffffffffu, again)) {
-        float top = vref;
-#pragma unroll
-        for (int gp = 0; gp < kGroups; ++gp) top = fmaxf(top, fmaxf(vs[0][gp], vs[1][gp]));
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        float vf = 1.f;
-        if (top > vref) {
-          const uint32_t bits = min((__float_as_uint(top) & 0x7f800000u) + 0x800000u, 0x7f000000u);
-          const float next = __uint_as_float(bits);
-          vf = vref / next;
-          vref = next;
-          vinv = 1.f / next;
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            float hi = fmaxf(x[nt][r], x[nt][r + 2]);
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-            const bool none = thr[nt][r] == -INFINITY;
-            float f = 1.f;
-            if (hi > -INFINITY && (none || hi > m[nt][r])) {
-              f = none ? 0.f : ex2_approx(m[nt][r] - hi);
-              m[nt][r] = hi;
-              thr[nt][r] = hi + 8.f;
-            }
-            l[nt][r] *= f;
-#pragma unroll
-            for (int gp = 0; gp < kGroups; ++gp) lo_sum[nt][gp][r] *= f;
-#pragma unroll
-            for (int j = 0; j < kVW; ++j)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                acc[j][i][nt][r] *= f * vf;
-                acc[j][i][nt][r + 2] *= f * vf;
-              }
+      const uint8_t* at = ring + stage * L::kBlock;
+      const uint32_t there = (present >> (2 * stage)) & 3u;
+      if (kFast == 2 && there == 3u && key0 + 32 <= all_see) {
+        kv4_tiles<D, NT, kFast, false>(at, places, smem + L::kOffQ, qf, qs, rs, lim, key0, any_sees, st);
+      } else {
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half)
+          if ((there >> half) & 1u) {
+            if (kFast == 1 && key0 + 16 * half + 16 <= all_see)
+              kv4_tiles<D, NT, 1, false>(at + half * T::kBytes, places, smem + L::kOffQ, qf, qs, rs, lim,
+                                         key0 + 16 * half, any_sees, st);
+            else
+              kv4_tiles<D, NT, 1, true>(at + half * T::kBytes, places, smem + L::kOffQ, qf, qs, rs, lim,
+                                        key0 + 16 * half, any_sees, st);
           }
       }
-      // ---- P, P s as B fragments, P mid
-      uint32_t pb[NT][kGroups][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float e[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          e[c] = ex2_approx(x[nt][c] - m[nt][c & 1]);
-          l[nt][c & 1] += e[c];
-        }
-#pragma unroll
-        for (int gp = 0; gp < kGroups; ++gp) {
-          float pv[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int i = c >> 1, r = c & 1;
-            pv[c] = e[c] * (vs[i][gp] * vinv);
-            float pm = e[c] * vm[i][gp];
-            if (masked && key[i] >= lim[nt][r]) pv[c] = pm = 0.f;
-            lo_sum[nt][gp][r] += pm;
-          }
-          pb[nt][gp][0] = transpose8(pack_f16x2(pv[0], pv[1]));
-          pb[nt][gp][1] = transpose8(pack_f16x2(pv[2], pv[3]));
-        }
+      __syncwarp();
+      key0 += kKv4Chunk;
+      if (++stage == kS) {
+        stage = 0;
+        parity ^= 1;
       }
-      // ---- O^T += V^T P^T
-#pragma unroll
-      for (int j = 0; j < kVW; ++j)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t sel = half ? 0x7632u : 0x5410u;
-          uint32_t a[4], c[4];
-          codes_f16(__byte_perm(vw[0][j], vw[1][j], sel), a);
-          codes_f16(__byte_perm(vw[2][j], vw[3][j], sel), c);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_f16(acc[j][2 * half][nt], a[0], a[1], c[0], c[1], pb[nt][j][0], pb[nt][j][1]);
-            mma_f16(acc[j][2 * half + 1][nt], a[2], a[3], c[2], c[3], pb[nt][j][0], pb[nt][j][1]);
-          }
-        }
     }
+    if (!ok && lane == 0)  // let the copies in flight land
+      for (int j = i; j < min(i + kS, n_blk); ++j)
+        drain_wait(bars + 8 * ((it + j) % kS), ((it + j) / kS) & 1, p.limit_ns);
+    it += n_blk;
+    __syncthreads();  // the ring is empty
+    if (*abort_flag) return;
 
     // ---- this warp's results to shared memory
+    const float vref = st.vinv == 0.f ? 0.f : 1.f / st.vinv;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        float sum = l[nt][r];
+        float sum = st.l[nt][r];
         float lo[kGroups];
 #pragma unroll
-        for (int gp = 0; gp < kGroups; ++gp) lo[gp] = lo_sum[nt][gp][r];
+        for (int gp = 0; gp < kGroups; ++gp) lo[gp] = st.lo_sum[nt][gp][r];
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
           sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -507,45 +736,54 @@ __global__ void __launch_bounds__(kKv4Warps * 32)
         const int row = 8 * nt + 2 * t + r;
         float* to = merge + (warp * L::kRows + row) * L::kPitch;
 #pragma unroll
-        for (int j = 0; j < kVW; ++j)
+        for (int j = 0; j < kVW; ++j) {
+          float v[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            to[64 * j + 8 * g + 2 * i] = fmaf(acc[j][i][nt][r], vref, lo[j]);
-            to[64 * j + 8 * g + 2 * i + 1] = fmaf(acc[j][i][nt][r + 2], vref, lo[j]);
+          for (int k = 0; k < 4; ++k) {
+            v[2 * k] = fmaf(st.acc[j][k][nt][r] * 0x1p24f, vref, lo[j]);
+            v[2 * k + 1] = fmaf(st.acc[j][k][nt][r + 2] * 0x1p20f, vref, lo[j]);
           }
+          *reinterpret_cast<float4*>(to + 64 * j + 8 * g) = make_float4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<float4*>(to + 64 * j + 8 * g + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        }
         if (g == 0) {
           // no key seen (a row of NaN scores has a NaN sum instead)
-          s_m[warp * L::kRows + row] = thr[nt][r] == -INFINITY && sum == 0.f ? -INFINITY : m[nt][r];
+          s_m[warp * L::kRows + row] =
+              st.m[nt][r] == -3.402823466e38f && sum == 0.f ? -INFINITY : st.m[nt][r];
           s_l[warp * L::kRows + row] = sum;
         }
       }
     __syncthreads();
+    // a warp takes every fourth row: a lane D / 32 channels
     const bool whole = c0 == 0 && c1 == rq.chunks;
     float* part = p.part + (2LL * cta + (u == u_begin && c0 > 0 ? 0 : 1)) * L::kPartFloats;
-    for (int idx = tid; idx < rows * D; idx += kKv4Warps * 32) {
-      const int r = idx / D, ch = idx % D;
-      float top = -INFINITY;
+    for (int r = warp; r < rows; r += kKv4Warps) {
+      float top = -INFINITY, sum = 0.f, f[kKv4Warps], o[D / 32] = {};
 #pragma unroll
       for (int w = 0; w < kKv4Warps; ++w) top = fmaxf(top, s_m[w * L::kRows + r]);
-      float o = 0.f, sum = 0.f;
 #pragma unroll
       for (int w = 0; w < kKv4Warps; ++w) {
         const float mw = s_m[w * L::kRows + r];
-        if (mw == -INFINITY) continue;
-        const float f = ex2_approx(mw - top);
-        o = fmaf(merge[(w * L::kRows + r) * L::kPitch + ch], f, o);
-        sum = fmaf(s_l[w * L::kRows + r], f, sum);
+        f[w] = mw == -INFINITY ? 0.f : ex2_approx(mw - top);
+        const float lw = s_l[w * L::kRows + r];
+        if (mw != -INFINITY) sum = fmaf(lw, f[w], sum);
+        float v[D / 32];
+        load_floats<D / 32>(merge + (w * L::kRows + r) * L::kPitch + lane * (D / 32), v);
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k)
+          if (mw != -INFINITY) o[k] = fmaf(v[k], f[w], o[k]);
       }
-      if (whole) {
-        kv4_store_row<D, NT>(p, rq, h, row0 + r, ch, o, top, sum);
-      } else {
-        part[r * D + ch] = o;
-        if (ch == 0) {
+      if (whole)
+        kv4_store_row<D>(p, rq, h, row0 + r, lane, o, top, sum);
+      else {
+        store_floats<D / 32>(part + r * D + lane * (D / 32), o);
+        if (lane == 0) {
           part[L::kRows * D + r] = top;
           part[L::kRows * (D + 1) + r] = sum;
         }
       }
     }
+    fence_proxy_async_smem();  // the next piece's copies follow these accesses
     __syncthreads();
     u += c1 - c0;
   }
@@ -553,41 +791,64 @@ __global__ void __launch_bounds__(kKv4Warps * 32)
 
 // Joins the partial results.  Block c looks at the start of CTA c + 1's range:
 // if it cuts a (request, row tile, head), and no earlier range start does, the
-// block owns that cut one and sums its pieces, left by the CTAs in order.
+// block owns that cut one and sums its pieces, left by the CTAs in order.  A
+// warp takes every fourth row; its lanes first find the pieces' weights.
 template <int D, int NT>
 __global__ void __launch_bounds__(kKv4Warps * 32)
     kv4_combine_kernel(const __grid_constant__ Kv4AttendParams p, int ctas) {
   using L = Kv4AttendLayout<D, NT>;
   __shared__ Kv4Shared sh;
-  const int cta = blockIdx.x + 1;
-  kv4_locate<L::kRows>(p, sh, [&](long long total) { return kv4_start(total, cta, ctas); });
+  const int cta = blockIdx.x + 1, lane = threadIdx.x & 31;
+  kv4_locate<L::kRows>(p, sh, cta, ctas);
   if (sh.found_b < 0) return;
-  const long long total = sh.total, cut = kv4_start(total, cta, ctas);
+  const Kv4Share share(sh.total, ctas);
+  const long long cut = share.start(cta);
   const Kv4Req rq = kv4_request<L::kRows>(p, sh.found_b);
-  const long long job = (cut - sh.found_excl) / rq.chunks;
+  const long long job = kv4_div(cut - sh.found_excl, rq.chunks);
   const long long u0 = sh.found_excl + job * rq.chunks, u1 = u0 + rq.chunks;
-  if (cut == u0 || kv4_start(total, cta - 1, ctas) > u0) return;
-  int last = cta;  // the CTA that holds the last unit
-  while (kv4_start(total, last + 1, ctas) < u1) ++last;
-  const int h = static_cast<int>(job % p.kv_heads);
-  const int row0 = static_cast<int>(job / p.kv_heads) * L::kRows;
+  if (cut == u0 || share.start(cta - 1) > u0) return;
+  // CTAs first .. last hold a piece each (none is empty: it starts below u1)
+  const int first = cta - 1;
+  int last = cta;
+  while (share.start(last + 1) < u1) ++last;
+  const int tile_row = static_cast<int>(kv4_div(job, p.kv_heads));
+  const int h = static_cast<int>(job - static_cast<long long>(tile_row) * p.kv_heads);
+  const int row0 = tile_row * L::kRows;
   const int rows = min(L::kRows, rq.n * p.group - row0);
-  for (int idx = threadIdx.x; idx < rows * D; idx += kKv4Warps * 32) {
-    const int r = idx / D, ch = idx % D;
-    float o = 0.f, sum = 0.f, top = -INFINITY;
-    for (int c = cta - 1; c <= last; ++c) {
-      // empty ranges (fewer units than CTAs) left nothing
-      if (kv4_start(total, c, ctas) == kv4_start(total, c + 1, ctas)) continue;
-      const float* part = p.part + (2LL * c + (kv4_start(total, c, ctas) > u0 ? 0 : 1)) * L::kPartFloats;
-      const float m = part[L::kRows * D + r];
-      if (m == -INFINITY) continue;
-      const float next = fmaxf(top, m);
-      const float fo = ex2_approx(top - next), fn = ex2_approx(m - next);
-      o = o * fo + part[r * D + ch] * fn;
-      sum = sum * fo + part[L::kRows * (D + 1) + r] * fn;
-      top = next;
+  // piece k of the cut one: the first CTA left it in its second place if it
+  // began there, all others in their first
+  auto piece = [&](int k) {
+    return p.part + (2LL * (first + k) + (k == 0 && share.start(first) <= u0 ? 1 : 0)) * L::kPartFloats;
+  };
+  const int n = last - first + 1;
+  for (int r = threadIdx.x >> 5; r < rows; r += kKv4Warps) {
+    float top = -INFINITY;
+    for (int k = lane; k < n; k += 32) top = fmaxf(top, piece(k)[L::kRows * D + r]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float sum = 0.f, o[D / 32] = {};
+    for (int k0 = 0; k0 < n; k0 += 32) {
+      float w = 0.f;
+      if (k0 + lane < n) {
+        const float m = piece(k0 + lane)[L::kRows * D + r];
+        if (m != -INFINITY) {
+          w = ex2_approx(m - top);
+          sum = fmaf(piece(k0 + lane)[L::kRows * (D + 1) + r], w, sum);
+        }
+      }
+      const int here = min(32, n - k0);
+#pragma unroll 4
+      for (int k = 0; k < here; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+        float v[D / 32];
+        load_floats<D / 32>(piece(k0 + k) + r * D + lane * (D / 32), v);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) o[c] = fmaf(v[c], wk, o[c]);
+      }
     }
-    kv4_store_row<D, NT>(p, rq, h, row0 + r, ch, o, top, sum);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    kv4_store_row<D>(p, rq, h, row0 + r, lane, o, top, sum);
   }
 }
 

@@ -93,12 +93,7 @@ fa_status store_params(fa::Kv4StoreParams* p, const void* k, const void* v, cons
 
 int attend_tiles(int max_tokens, int group) {
   const long long rows = static_cast<long long>(max_tokens) * group;
-  return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
-}
-
-template <int D, int NT>
-int attend_ctas(int dev) {
-  return sm_count(dev) * (NT == 1 ? 4 : NT == 2 ? 3 : 2);
+  return rows <= 24 ? static_cast<int>((rows + 7) / 8) : 4;
 }
 
 template <int D, int NT>
@@ -111,7 +106,7 @@ fa_status launch_attend(const fa::Kv4AttendParams& p, cudaStream_t st) {
     if (!set_smem(fa::kv4_attend_kernel<D, NT>, L::kBytes)) return FA_ERR_CUDA;
     attr_set[dev] = true;
   }
-  const int ctas = attend_ctas<D, NT>(dev);
+  const int ctas = sm_count(dev) * L::kCtas;
   {
     LaunchTimer timer(st, FA_KERNEL_KV4_ATTEND);
     fa::kv4_attend_kernel<D, NT><<<ctas, fa::kKv4Warps * 32, L::kBytes, st>>>(p);
@@ -127,8 +122,8 @@ fa_status launch_attend(const fa::Kv4AttendParams& p, cudaStream_t st) {
 size_t attend_workspace(int d, int nt) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
-  const size_t ctas = static_cast<size_t>(sm_count(dev)) * (nt == 1 ? 4 : nt == 2 ? 3 : 2);
-  return ctas * 2 * static_cast<size_t>(8 * nt) * (d + 2) * sizeof(float);
+  const size_t per_cta = (nt == 1 ? fa::Kv4AttendLayout<128, 1>::kCtas : fa::Kv4AttendLayout<128, 2>::kCtas) * 2;
+  return static_cast<size_t>(sm_count(dev)) * per_cta * (8 * nt) * (d + 2) * sizeof(float);
 }
 
 }  // namespace
@@ -347,13 +342,18 @@ fa_status fa_kv4_attention(const void* q, const void* cache, const int* block_ta
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.causal = causal != 0;
   p.is_half = dtype == FA_FP16;
+  p.limit_ns = kWaitLimitNs;
+  p.page_tiles = fa::FastDiv::of(static_cast<uint32_t>(page_size / 16));
+  p.by_group = fa::FastDiv::of(static_cast<uint32_t>(p.group));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d == 64)
     return nt == 1   ? launch_attend<64, 1>(p, s)
            : nt == 2 ? launch_attend<64, 2>(p, s)
+           : nt == 3 ? launch_attend<64, 3>(p, s)
                      : launch_attend<64, 4>(p, s);
   return nt == 1   ? launch_attend<128, 1>(p, s)
          : nt == 2 ? launch_attend<128, 2>(p, s)
+         : nt == 3 ? launch_attend<128, 3>(p, s)
                    : launch_attend<128, 4>(p, s);
 }
 

@@ -83,9 +83,9 @@ def attention(q, cache, table, lengths, cu, causal, scale):
       * scores: fp32 sums of at most 128 products of a code with q and a few
         more operations: 2^-17 of the sum of the terms' sizes, eta; it moves P by
         the same relative amount;
-      * P s in fp16: 2^-11 of P times at most 8 s a key, and, below fp16's
-        smallest normal number, 2^-25 of the largest 8 s a key (the sum of P is at
-        least 1 at that scale);
+      * P s in fp16: 2^-11 of P times at most 15 s a key, and, below fp16's
+        smallest normal number, 2^-25 of the largest 15 s a key, twice that if s is
+        half its reference (the sum of P is at least 1 at that scale);
       * the output's type: u |O|.
     """
     T, H, d = q.shape
@@ -123,7 +123,7 @@ def attention(q, cache, table, lengths, cu, causal, scale):
                 size = (qq.abs() @ (k.abs() + 2 * k8).T * abs(scale)).masked_fill(hidden, 0.0)
                 eta = 2.0 ** -17 * size.amax(1, keepdim=True)
                 v8 = torch.where(hidden.all(0)[:, None], 0.0, v8)
-                to = (u * oo.abs() + 2.0 ** -11 * (p @ v8) + n * 2.0 ** -25 * v8.amax() +
+                to = (u * oo.abs() + 2.0 ** -11 * (p @ v8) * 15 / 8 + n * 2.0 ** -24 * v8.amax() * 15 / 8 +
                       eta * (p @ vz.abs() + oo.abs()) + 2.0 ** -20 * (p @ (vz.abs() + v8)))
                 tl = eta[:, 0] + 2.0 ** -20 + 2.0 ** -22 * ll.abs()
             shape = (new, H // G)
