@@ -6,18 +6,21 @@
 kernels with every TMA coordinate, TMEM column range and directly indexed
 global address checked before use (a failed check is reported through the
 device error word, see ``fa_check_device_error``).  Point the binding at it
-with the ``FA_LIBRARY`` environment variable.
+with the ``FA_LIBRARY`` environment variable.  The release build also compiles
+``_fa_binding.so`` (csrc/binding.cpp, host code) with g++ against torch.
 """
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libfa_b200.so")
+BINDING = os.path.join(PKG, "_fa_binding.so")  # Python extension module, host code only
 DEBUG_LIB = os.path.join(PKG, "libfa_b200_debug.so")
 SOURCES = ["fa_api.cu"]
 HEADERS = ["sm100.cuh", "common.cuh", "fwd.cuh", "bwd.cuh", "bwd_main.cuh", "dq_pass.cuh", "kv_outer.cuh",
@@ -49,8 +52,34 @@ def _stale(lib: str) -> bool:
     return any(os.path.getmtime(p) > t for p in deps if os.path.exists(p))
 
 
+def _build_binding(force: bool, verbose: bool):
+    """csrc/binding.cpp: the Python module between torch tensors and the C ABI."""
+    src = os.path.join(CSRC, "binding.cpp")
+    deps = [src, os.path.join(ROOT, "include", "fa.h")]
+    if not force and os.path.exists(BINDING) and \
+            all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
+        return
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(base, "include"),
+           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), src, "-o", tmp,
+           "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
+           "-ltorch_cuda", "-lc10_cuda", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False, extra=(), debug: bool = False) -> str:
     lib = DEBUG_LIB if debug else LIB
+    if not debug:
+        _build_binding(force, verbose)
     if not force and not _stale(lib):
         return lib
     tmp = lib + ".tmp"

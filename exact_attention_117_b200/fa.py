@@ -1,14 +1,15 @@
 """Python binding of the C ABI in include/fa.h (argument marshalling only).
 
-Every step of the attention computation runs in the CUDA library
-``libfa_b200.so``; this module only checks tensor properties, takes device
-pointers and the current stream from torch, and turns status codes into
-exceptions.  There is no fallback: if the library is missing or not built for
+Every step of the computation runs in the CUDA library ``libfa_b200.so``; this
+module only checks tensor properties, takes device pointers and the current
+stream from torch, and turns status codes into exceptions (through ctypes, the
+rotary and 4-bit cache calls through the extension module of csrc/binding.cpp).  There is no fallback: if the library is missing or not built for
 this GPU, every call raises.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
 from typing import NamedTuple, Optional
@@ -30,6 +31,7 @@ KERNELS = ("fwd", "bwd_pre", "bwd_main", "bwd_dq", "fwd_combine", "fwd_kv_outer"
            "kv4_plan", "kv4_append", "kv4_gather", "kv4_attend", "kv4_combine")
 
 _lib = None
+_native = None  # the extension module of csrc/binding.cpp, bound to _lib
 
 
 class FaError(RuntimeError):
@@ -97,6 +99,26 @@ def load() -> ctypes.CDLL:
     lib.fa_version.argtypes = []
     _lib = lib
     return lib
+
+
+def _load_native():
+    """The extension module with the serving calls, bound to the loaded library
+    (raises if it has not been built)."""
+    global _native
+    if _native is None:
+        lib = load()
+        path = os.path.join(_HERE, "_fa_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"binding not built: {path} is missing "
+                               "(run __graft_entry__.build())")
+        spec = importlib.util.spec_from_file_location("_fa_binding", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.fa_rotary, lib.fa_kv4_plan, lib.fa_kv4_append, lib.fa_kv4_gather,
+            lib.fa_kv4_attention_workspace_size, lib.fa_kv4_attention)))
+        _native = module
+    return _native
 
 
 def _check(status: int, where: str):
@@ -273,19 +295,8 @@ def backward_noalloc(q, k, v, o, lse, do, causal: bool = False, scale: Optional[
 
 
 # ------------------------------------------------------------ rotary positions
-_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # fa_dtype
-
-
-def _check_here(*ts: torch.Tensor):
-    """Every tensor is on the current device (whose stream the call uses)."""
-    here = torch.cuda.current_device()
-    for t in ts:
-        if not t.is_cuda or t.get_device() != here:
-            raise ValueError("tensors must be on the current CUDA device")
-
-
-def _longs(*values: int):
-    return (ctypes.c_longlong * len(values))(*values)
+def _stream_arg(stream):
+    return None if stream is None else int(stream.cuda_stream)
 
 
 def rotary_frequencies(rotary_dim: int, base: float = 10000.0, factor: float = 1.0,
@@ -316,45 +327,6 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, factor: float = 1
     return f.to(device), amplitude
 
 
-def _rotary(q, k, positions, inv_freq, interleaved, amplitude, out_q, out_k, stream, inverse,
-            where):
-    if q.dim() != 4 or q.stride(3) != 1 or q.dtype not in _DTYPES:
-        raise ValueError("expected bf16, fp16 or fp32 [B, H, N, d] tensors, d contiguous")
-    B, H, N, d = q.shape
-    out_q = torch.empty_like(q) if out_q is None else out_q
-    k_heads = 0
-    if k is not None:
-        out_k = torch.empty_like(k) if out_k is None else out_k
-        k_heads = k.shape[1] if k.dim() == 4 else 0
-        if (k.dim() != 4 or k.dtype != q.dtype or k.shape[0] != B or k.shape[2:] != q.shape[2:]
-                or k.stride(3) != 1 or out_k.shape != k.shape or out_k.dtype != k.dtype
-                or out_k.stride(3) != 1):
-            raise ValueError("k and its output must match q's [B, ., N, d], dtype and layout")
-    elif out_k is not None:
-        raise ValueError("an output for k without k")
-    if out_q.shape != q.shape or out_q.dtype != q.dtype or out_q.stride(3) != 1:
-        raise ValueError("the output must have q's shape, dtype and a contiguous d")
-    if positions.dtype not in (torch.int32, torch.int64) or \
-            tuple(positions.shape) not in ((N,), (B, N)) or \
-            (N > 1 and positions.stride(-1) != 1):
-        raise ValueError("positions must be int32 or int64 [N] or [B, N], N contiguous")
-    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
-        raise ValueError("inv_freq must be a contiguous fp64 vector")
-    ts = (q, out_q, positions, inv_freq) + (() if k is None else (k, out_k))
-    _check_here(*ts)
-    for t in (out_q,) if k is None else (out_q, out_k):
-        if any(t.stride(i) == 0 and t.shape[i] > 1 for i in range(3)):
-            raise ValueError("outputs must not overlap themselves")
-    strides = _longs(*q.stride()[:3], *out_q.stride()[:3],
-                     *((0,) * 6 if k is None else (*k.stride()[:3], *out_k.stride()[:3])))
-    _check(load().fa_rotary(_ptr(q), _ptr(k), _ptr(out_q), _ptr(out_k), B, H, k_heads, N, d,
-                            strides, _ptr(positions), positions.dtype == torch.int64,
-                            positions.stride(0) if positions.dim() == 2 else 0, _ptr(inv_freq),
-                            2 * inv_freq.numel(), bool(interleaved), float(amplitude), inverse,
-                            _DTYPES[q.dtype], _stream_ptr(stream)), where)
-    return out_q, out_k
-
-
 def rotary(q, k, positions, inv_freq, interleaved: bool = False, amplitude: float = 1.0,
            out_q=None, out_k=None, stream=None):
     """Rotary positions of queries ``[B, H, N, d]`` and keys ``[B, Hk, N, d]``
@@ -363,16 +335,22 @@ def rotary(q, k, positions, inv_freq, interleaved: bool = False, amplitude: floa
     ``positions``: int32 or int64 ``[N]`` or ``[B, N]``.  The first
     ``2 * len(inv_freq)`` channels turn, in pairs ``(i, i + len(inv_freq))`` or,
     ``interleaved``, ``(2i, 2i + 1)``.  Outputs may be the inputs."""
-    return _rotary(q, k, positions, inv_freq, interleaved, amplitude, out_q, out_k, stream, 0,
-                   "fa_rotary")
+    st, out_q, out_k = (_native or _load_native()).rotary(
+        q, k, positions, inv_freq, interleaved, amplitude, out_q, out_k, _stream_arg(stream), False)
+    if st:
+        raise FaError(st, "fa_rotary")
+    return out_q, out_k
 
 
 def rotary_backward(dq, dk, positions, inv_freq, interleaved: bool = False,
                     amplitude: float = 1.0, out_q=None, out_k=None, stream=None):
     """Gradients of :func:`rotary`'s inputs from those of its outputs (the same
     arguments otherwise)."""
-    return _rotary(dq, dk, positions, inv_freq, interleaved, amplitude, out_q, out_k, stream, 1,
-                   "fa_rotary")
+    st, out_q, out_k = (_native or _load_native()).rotary(
+        dq, dk, positions, inv_freq, interleaved, amplitude, out_q, out_k, _stream_arg(stream), True)
+    if st:
+        raise FaError(st, "fa_rotary")
+    return out_q, out_k
 
 
 # ------------------------------------------------------------ 4-bit KV cache
@@ -393,19 +371,6 @@ def kv4_cache(pages: int, kv_heads: int, page_size: int, d: int, device="cuda"):
                        device=device)
 
 
-def _cache_dims(cache, d: int):
-    if cache.dtype != torch.uint8 or cache.dim() != 4 or not cache.is_contiguous() or \
-            cache.shape[3] != 18 * d:
-        raise ValueError("the cache must be contiguous uint8 [pages, kv_heads, page / 16, 18 d]")
-    return cache.shape[0], cache.shape[1], cache.shape[2] * 16
-
-
-def _check_ints(*ts):
-    for t, dtype, shape in ts:
-        if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError(f"expected a contiguous {dtype} tensor of shape {shape}")
-
-
 def kv4_plan(lengths, new_lengths, block_table, free_pages, free_range, page_size: int,
              max_tokens: int, lengths_out=None, free_range_out=None, stream=None) -> Kv4Plan:
     """Pages, slots and positions of a step, on the device: requests go from
@@ -414,81 +379,30 @@ def kv4_plan(lengths, new_lengths, block_table, free_pages, free_range, page_siz
     ``free_range[0]`` to ``free_range[1]``, int64) are updated in place;
     lengths and range too if they are passed as their own outputs.  See
     ``fa_kv4_plan`` in include/fa.h for the statuses."""
-    if lengths.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
-        raise ValueError("expected lengths [requests], block_table [requests, width], "
-                         "free_pages [pages]")
-    R, i32, i64 = lengths.shape[0], torch.int32, torch.int64
-    dev = lengths.device
-    lengths_out = torch.empty_like(lengths) if lengths_out is None else lengths_out
-    free_range_out = torch.empty_like(free_range) if free_range_out is None else free_range_out
-    _check_ints((lengths, i32, (R,)), (new_lengths, i32, (R,)), (lengths_out, i32, (R,)),
-                (free_pages, i32, tuple(free_pages.shape)), (free_range, i64, (2,)),
-                (free_range_out, i64, (2,)))
-    if block_table.dtype != i32 or block_table.shape[0] != R or block_table.stride(1) != 1:
-        raise ValueError("block_table must be int32 [requests, width] with contiguous rows")
-    _check_here(lengths, new_lengths, block_table, free_pages, free_range, lengths_out,
-                free_range_out)
-    max_tokens = int(max_tokens)
-    cu = torch.empty(R + 1, dtype=i32, device=dev)
-    slots = torch.empty(max(max_tokens, 0), dtype=i64, device=dev)
-    positions = torch.empty(max(max_tokens, 0), dtype=i32, device=dev)
-    status = torch.empty(1, dtype=i32, device=dev)
-    _check(load().fa_kv4_plan(_ptr(lengths), _ptr(new_lengths), _ptr(block_table),
-                              block_table.stride(0), block_table.shape[1], _ptr(free_pages),
-                              free_pages.shape[0], _ptr(free_range), R, int(page_size),
-                              max_tokens, _ptr(lengths_out), _ptr(free_range_out), _ptr(cu),
-                              _ptr(slots), _ptr(positions), _ptr(status), _stream_ptr(stream)),
-           "fa_kv4_plan")
-    return Kv4Plan(lengths_out, cu, slots, positions, status, free_range_out)
-
-
-def _check_store(k, v, slots):
-    if k.dim() != 3 or k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or \
-            v.shape != k.shape or k.stride(2) != 1 or v.stride(2) != 1:
-        raise ValueError("keys and values must be bf16 [tokens, kv_heads, d], d contiguous")
-    _check_ints((slots, torch.int64, (k.shape[0],)))
+    st, *out = (_native or _load_native()).plan(
+        lengths, new_lengths, block_table, free_pages, free_range, page_size, max_tokens,
+        lengths_out, free_range_out, _stream_arg(stream))
+    if st:
+        raise FaError(st, "fa_kv4_plan")
+    return Kv4Plan(*out)
 
 
 def kv4_append(k, v, cache, slots, stream=None):
     """Quantises keys and values (bf16 ``[tokens, kv_heads, d]``, d contiguous)
     into ``slots`` (int64, ``page * page_size + place``; -1 skips, and no slot
     twice) of the cache."""
-    _check_store(k, v, slots)
-    T, heads, d = k.shape
-    pages, kv_heads, page_size = _cache_dims(cache, d)
-    if heads != kv_heads:
-        raise ValueError("keys and the cache differ in kv_heads")
-    _check_here(k, v, cache, slots)
-    _check(load().fa_kv4_append(_ptr(k), _ptr(v), _ptr(cache), _ptr(slots), T, heads, d, pages,
-                                page_size, _longs(*k.stride()[:2], *v.stride()[:2]),
-                                _stream_ptr(stream)), "fa_kv4_append")
+    st = (_native or _load_native()).append(k, v, cache, slots, _stream_arg(stream))
+    if st:
+        raise FaError(st, "fa_kv4_append")
 
 
 def kv4_gather(cache, slots, out_k=None, out_v=None, stream=None):
     """The values that the cache holds for ``slots``: bf16 keys and values
     ``[tokens, kv_heads, d]``; zeros for slots outside the cache."""
-    if cache.dim() != 4 or cache.shape[3] % 18:
-        raise ValueError("the cache must be contiguous uint8 [pages, kv_heads, page / 16, 18 d]")
-    d = cache.shape[3] // 18
-    pages, heads, page_size = _cache_dims(cache, d)
-    shape = (slots.shape[0] if slots.dim() == 1 else -1, heads, d)
-    if shape[0] < 0:
-        raise ValueError("slots must be a vector")
-    if out_k is None:
-        out_k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
-    if out_v is None:
-        out_v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
-    if tuple(out_k.shape) != shape:
-        raise ValueError("outputs must be bf16 [tokens, kv_heads, d]")
-    _check_store(out_k, out_v, slots)
-    _check_here(cache, slots, out_k, out_v)
-    for t in (out_k, out_v):
-        if any(t.stride(i) == 0 and t.shape[i] > 1 for i in range(2)):
-            raise ValueError("outputs must not overlap themselves")
-    _check(load().fa_kv4_gather(_ptr(cache), _ptr(slots), _ptr(out_k), _ptr(out_v), shape[0],
-                                heads, d, pages, page_size,
-                                _longs(*out_k.stride()[:2], *out_v.stride()[:2]),
-                                _stream_ptr(stream)), "fa_kv4_gather")
+    st, out_k, out_v = (_native or _load_native()).gather(cache, slots, out_k, out_v,
+                                                          _stream_arg(stream))
+    if st:
+        raise FaError(st, "fa_kv4_gather")
     return out_k, out_v
 
 
@@ -507,37 +421,11 @@ def kv4_attention(q, cache, block_table, lengths, cu_tokens, max_tokens: int,
     (int32 ``[requests, width]``) lists its pages.  ``max_tokens``: an upper
     bound on a request's query rows (it chooses the kernel).  Rows that see no
     key get zeros and -inf; rows of no request are left as they are."""
-    if q.dim() != 3 or q.dtype not in (torch.bfloat16, torch.float16) or q.stride(2) != 1:
-        raise ValueError("queries must be bf16 or fp16 [tokens, heads, d], d contiguous")
-    T, heads, d = q.shape
-    pages, kv_heads, page_size = _cache_dims(cache, d)
-    if heads % kv_heads:
-        raise ValueError("the number of heads must be a multiple of the cache's")
-    R = block_table.shape[0] if block_table.dim() == 2 else -1
-    if block_table.dtype != torch.int32 or R < 0 or block_table.stride(1) != 1:
-        raise ValueError("block_table must be int32 [requests, width] with contiguous rows")
-    _check_ints((lengths, torch.int32, (R,)), (cu_tokens, torch.int32, (R + 1,)))
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    out = torch.empty_like(q) if out is None else out
-    if lse is None:
-        lse = torch.empty((T, heads), dtype=torch.float32, device=q.device)
-    if out.shape != q.shape or out.dtype != q.dtype or out.stride(2) != 1 or \
-            any(out.stride(i) == 0 and out.shape[i] > 1 for i in range(2)):
-        raise ValueError("the output must have q's shape, dtype and a contiguous d")
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (T, heads) or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous fp32 [tokens, heads] tensor")
-    if workspace is None:
-        need = kv4_attention_workspace_size(heads, kv_heads, d, int(max_tokens))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    _check_here(q, cache, block_table, lengths, cu_tokens, out, lse, workspace)
-    _check(load().fa_kv4_attention(_ptr(q), _ptr(cache), _ptr(block_table), _ptr(lengths),
-                                   _ptr(cu_tokens), _ptr(out), _ptr(lse), R, T, heads, kv_heads,
-                                   d, pages, page_size, block_table.shape[1],
-                                   block_table.stride(0),
-                                   _longs(*q.stride()[:2], *out.stride()[:2]), int(max_tokens),
-                                   bool(causal), float(scale), _DTYPES[q.dtype],
-                                   _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                   _stream_ptr(stream)), "fa_kv4_attention")
+    st, out, lse = (_native or _load_native()).attention(
+        q, cache, block_table, lengths, cu_tokens, max_tokens, causal, scale, out, lse, workspace,
+        _stream_arg(stream))
+    if st:
+        raise FaError(st, "fa_kv4_attention")
     return out, lse
 
 

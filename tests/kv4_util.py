@@ -1,10 +1,16 @@
 """Plain 64-bit restatements of the rotary positions and of the 4-bit cache,
 for the tests: torch on whatever device the inputs are on, no product code."""
+import ctypes
 import math
 
 import torch
 
 GROUP = 64
+
+
+def longs(*values):
+    """A C array of long long, as the strides of the C calls."""
+    return (ctypes.c_longlong * len(values))(*values)
 
 
 def rotary(x, positions, inv_freq, interleaved, amplitude, inverse=False):

@@ -18,7 +18,7 @@ def _raw(q=P, cache=P, table=P, lens=P, cu=P, o=P, lse=P, R=2, T=3, H=4, G=2, d=
     if size is None:
         size = lib.fa_kv4_attention_workspace_size(max(H, 1), max(G, 1), 64, max(most, 1)) or 1 << 30
     return lib.fa_kv4_attention(q, cache, table, lens, cu, o, lse, R, T, H, G, d, pages, page, width,
-                                stride, fa._longs(*strides), most, 1, scale, dtype, ws, size, None)
+                                stride, ref.longs(*strides), most, 1, scale, dtype, ws, size, None)
 
 
 def test_refusals():

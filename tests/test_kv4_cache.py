@@ -33,7 +33,7 @@ def test_plan_refusals():
 
 def _store_raw(call, k=P, v=P, cache=P, slots=P, T=3, H=2, d=64, pages=4, page=16, strides=(128, 64, 128, 64)):
     lib = fa.load()
-    st = fa._longs(*strides)
+    st = ref.longs(*strides)
     if call == "append":
         return lib.fa_kv4_append(k, v, cache, slots, T, H, d, pages, page, st, None)
     return lib.fa_kv4_gather(cache, slots, k, v, T, H, d, pages, page, st, None)

@@ -13,7 +13,7 @@ P = 0x10000  # fake, never-dereferenced, 16-byte aligned address
 def _raw(q=P, k=P, qo=P, ko=P, B=1, Hq=1, Hk=1, N=4, d=64, strides=None, pos=P, p64=0, ps=0,
          inv=P, rot=64, inter=0, amp=1.0, dtype=0):
     st = strides or [256, 256, 64] * 4
-    return fa.load().fa_rotary(q, k, qo, ko, B, Hq, Hk, N, d, fa._longs(*st), pos, p64, ps, inv,
+    return fa.load().fa_rotary(q, k, qo, ko, B, Hq, Hk, N, d, ref.longs(*st), pos, p64, ps, inv,
                                rot, inter, amp, 0, dtype, None)
 
 
