@@ -62,27 +62,78 @@ struct Kv4StoreParams {
   uint8_t* cache;
   const long long* slots;     // page * page_size + offset in the page
   long long n_slots;          // slots of the cache
-  long long n_items;          // tokens * heads * 2 * (d / 8)
-  int heads, page_size;
+  long long tokens;
+  int heads, page_tiles, block_tokens;
+  FastDiv by_page_tiles, by_lanes;  // tiles of a page, `lanes`
+  int lanes, side_by_side;  // threads that share a token, tokens walked side by side
 };
 
-// Byte offset of the row parts of a (slot, head): tile base and row.
+// A block of append or gather takes up to kStoreTokens tokens.  A thread keeps
+// two adjacent code words (16 channels of a K or V head) and walks the block's
+// tokens with them, two at a time so that their loads are in flight together;
+// where a token has fewer words than the block threads, several tokens are
+// walked side by side.  The slots' places in the cache are worked out once, in shared memory.
+constexpr int kStoreThreads = 256;
+constexpr int kStoreTokens = 16;
+constexpr int kStoreBatch = 2;
+
+struct StorePlaces {
+  long long tile[kStoreTokens];  // byte offset of head 0's tile, -1: outside
+  int row[kStoreTokens];
+};
 template <int D>
-__device__ __forceinline__ long long kv4_tile_at(const Kv4StoreParams& p, long long slot, int h) {
-  const long long page = slot / p.page_size;
-  const int off = static_cast<int>(slot - page * p.page_size);
-  return ((page * p.heads + h) * (p.page_size / 16) + off / 16) * Kv4Tile<D>::kBytes;
+__device__ __forceinline__ int store_places(const Kv4StoreParams& p, long long token0,
+                                            StorePlaces& sp) {
+  const int n = static_cast<int>(min(static_cast<long long>(p.block_tokens), p.tokens - token0));
+  if (static_cast<int>(threadIdx.x) < n) {
+    const long long slot = p.slots[token0 + threadIdx.x];
+    long long at = -1;
+    if (slot >= 0 && slot < p.n_slots) {
+      const uint32_t tile = static_cast<uint32_t>(slot >> 4);  // below 2^31
+      const uint32_t page = p.by_page_tiles(tile);
+      at = (static_cast<long long>(tile) + static_cast<long long>(page) * (p.heads - 1) * p.page_tiles) *
+           Kv4Tile<D>::kBytes;
+    }
+    sp.tile[threadIdx.x] = at;
+    sp.row[threadIdx.x] = static_cast<int>(slot & 15);
+  }
+  __syncthreads();
+  return n;
 }
 
-__device__ __forceinline__ float group8_min(float v) {
-#pragma unroll
-  for (int o = 1; o < 8; o <<= 1) v = fminf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+// The pair of words a thread keeps: where it lies in x and in a tile.
+template <int D>
+struct StoreWords {
+  int value, h, word, next;  // next: bytes from the first word to the second
+  long long in_cache;        // of row 0
+  __device__ __forceinline__ StoreWords(const Kv4StoreParams& p, int i) {
+    using L = Kv4Tile<D>;
+    const int half = p.heads * (D / 16);
+    value = i >= half;
+    const int of_kind = i - (value ? half : 0);
+    h = of_kind / (D / 16);
+    word = of_kind % (D / 16) * 2;
+    next = value ? D / 16 : D / 8;
+    in_cache = static_cast<long long>(h) * p.page_tiles * L::kBytes +
+               (value ? L::kOffV : L::kOffK) + 4 * L::place(word, value != 0);
+  }
+  // of a row's parameters, from the row's first word
+  __device__ __forceinline__ int par(int row) const {
+    using L = Kv4Tile<D>;
+    return 16 * L::kRow - 4 * L::place(word, value != 0) - row * (L::kRow - L::kPar) + (word >> 3) * 4;
+  }
+};
+
+// Lower and higher of two pairs of bf16; a NaN wins.
+__device__ __forceinline__ uint32_t min_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
-__device__ __forceinline__ float group8_max(float v) {
-#pragma unroll
-  for (int o = 1; o < 8; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 // Smallest bf16 s with 15 s >= span (span > 0, finite): the product by 1/15
@@ -94,80 +145,118 @@ __device__ __forceinline__ float kv4_scale(float span) {
   return __uint_as_float(bits);
 }
 
-// Quantises keys and values into the cache.  One thread takes the 8 channels
-// of one code word; 8 neighbouring lanes hold a group of 64 channels and find
-// its lowest and highest value by shuffles.
+// Quantises keys and values into the cache: 4 neighbouring lanes hold a group
+// of 64 channels and find its lowest and highest value by shuffles.
 //
 // lowest = the minimum (a bf16 already), scale = the smallest bf16 with 15
 // scale >= span, n = floor((x - lowest) / scale + 1/2).  The comparisons are
-// exact: x - lowest is rounded down and the span up, and both are compared
-// with (n + 1/2) scale and 15 scale, which 32 bits hold exactly; the quotient
-// by the reciprocal only proposes n.  A group with an infinity, a NaN or a
-// span beyond the largest float reads back as NaN.
+// exact.  With dist = x - lowest rounded down and a reciprocal a little too
+// small, n0 = dist * reciprocal to the nearest is n or n - 1; it is n - 1 just
+// where dist - n0 scale, rounded down, is not below scale / 2: every border
+// (n0 + 1/2) scale is a 32-bit number, and rounding down moves no number across
+// it.  Four codes are packed as one exact 32-bit float.
+// A group with an infinity, a NaN or a span beyond the largest float reads back
+// as NaN.
+//
+// Bound by instructions as much as by memory: about 8 an element besides the
+// reduction.
 template <int D>
-__global__ void __launch_bounds__(256) kv4_append_kernel(const __grid_constant__ Kv4StoreParams p) {
+__device__ __forceinline__ void append_words(const Kv4StoreParams& p, const StoreWords<D>& w,
+                                             long long tile, int row, const uint32_t (&r)[8]) {
   using L = Kv4Tile<D>;
-  constexpr int kWords = D / 8;
-  const long long id = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const bool live = id < p.n_items;
-  const int word = static_cast<int>(id % kWords);
-  const long long rest = live ? id / kWords : 0;
-  const int h = static_cast<int>(rest % p.heads);
-  const long long tk = rest / p.heads;
-  const int value = static_cast<int>(tk & 1);
-  const long long token = tk >> 1;
-  const long long slot = live ? p.slots[token] : -1;
-  const bool in = slot >= 0 && slot < p.n_slots;
-
-  float x[8] = {};
-  if (in) {
-    const uint4 raw = *reinterpret_cast<const uint4*>(p.x[value] + token * p.st[value] +
-                                                      h * p.sh[value] + word * 8);
-    const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
+  // (lowest, -highest) of the group as a pair: one shuffle serves both
+  uint32_t least = r[0], most = r[0];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = bf16_lo(r[i]);
-      x[2 * i + 1] = bf16_hi(r[i]);
-    }
+  for (int i = 1; i < 8; ++i) {
+    least = min_nan_bf16x2(least, r[i]);
+    most = max_nan_bf16x2(most, r[i]);
   }
-  float lo = x[0], hi = x[0], odd = 0.f;
+  least = min_nan_bf16x2(least, __byte_perm(least, 0, 0x1032));
+  most = max_nan_bf16x2(most, __byte_perm(most, 0, 0x1032)) ^ 0x80008000u;
+  uint32_t ends = __byte_perm(least, most, 0x5410);
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1)
+    ends = min_nan_bf16x2(ends, __shfl_xor_sync(0xffffffffu, ends, o));
+  float lo = bf16_lo(ends);
+  const float span = __fsub_ru(-bf16_hi(ends), lo);
+  const bool bad = !isfinite(span);
+  float scale = bad || span == 0.f ? 0.f : kv4_scale(span);
+  const uint32_t par = (__float_as_uint(scale) >> 16) |
+                       ((bad ? 0x7fc00000u : __float_as_uint(lo)) & 0xffff0000u);
+
+  float x[16];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-    odd = fmaxf(odd, isfinite(x[i]) ? 0.f : 1.f);
+    x[2 * i] = bf16_lo(r[i]);
+    x[2 * i + 1] = bf16_hi(r[i]);
   }
-  lo = group8_min(lo);
-  hi = group8_max(hi);
-  odd = group8_max(odd);
-  const float span = __fsub_ru(hi, lo);
-  const bool bad = odd != 0.f || !isfinite(span);
-  const float scale = bad || span == 0.f ? 0.f : kv4_scale(span);
-
-  uint32_t code = 0;
-  if (scale > 0.f) {
-    // groups of tiny values are lifted (exactly) so that 1 / scale is finite
-    const float lift = scale < 0x1p-60f ? 0x1p100f : 1.f;
-    const float s = scale * lift, inv = 1.f / s;
+  if (scale < 0x1p-60f && scale > 0.f) {
+    // a group of tiny values is lifted (exactly) so that 1 / scale is finite
+    scale *= 0x1p100f;
+    lo *= 0x1p100f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float dist = __fsub_rd(x[i], lo) * lift;
-      float n = fminf(floorf(dist * inv + 0.5f), 15.f);
-      if (dist < (n - 0.5f) * s) n -= 1.f;
-      if (dist >= (n + 0.5f) * s) n += 1.f;
-      code |= static_cast<uint32_t>(fminf(fmaxf(n, 0.f), 15.f)) << (4 * i);
-    }
+    for (int i = 0; i < 16; ++i) x[i] *= 0x1p100f;
   }
-  if (!in) return;
-  uint8_t* tile = p.cache + kv4_tile_at<D>(p, slot, h);
-  const int row = static_cast<int>(slot & 15);
-  *reinterpret_cast<uint32_t*>(tile + (value ? L::kOffV : L::kOffK) + row * L::kRow +
-                               4 * L::place(word, value != 0)) = code;
-  if ((word & 7) == 0) {
-    const uint32_t lo_bits = bad ? 0x7fc00000u : __float_as_uint(lo);
-    *reinterpret_cast<uint32_t*>(tile + (value ? L::kOffVPar : L::kOffKPar) + row * L::kPar +
-                                 (word >> 3) * 4) =
-        (__float_as_uint(scale) >> 16) | (lo_bits & 0xffff0000u);
+  // (scale 0: the products by a zero reciprocal leave every code 0, and half a
+  // step of infinity leaves it there)
+  const float inv = scale > 0.f ? __fdividef(1.f - 0x1p-20f, scale) : 0.f;
+  const float half = scale > 0.f ? 0.5f * scale : INFINITY;
+  float four[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 15; i >= 0; --i) {
+    const float dist = __fsub_rd(x[i], lo);
+    float n = fmaf(dist, inv, 0x1p23f) - 0x1p23f;  // to the nearest whole number
+    if (__fmaf_rd(-n, scale, dist) >= half) n += 1.f;
+    four[i >> 2] = fmaf(four[i >> 2], 16.f, n);
+  }
+  // 2^23 + a whole number below 2^16: its bits are the number's
+  uint32_t code[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    code[i] = bad ? 0u
+                  : __byte_perm(__float_as_uint(four[2 * i] + 0x1p23f),
+                                __float_as_uint(four[2 * i + 1] + 0x1p23f), 0x5410);
+  if (tile < 0) return;
+  uint8_t* at = p.cache + tile + w.in_cache + row * L::kRow;
+  *reinterpret_cast<uint32_t*>(at) = code[0];
+  *reinterpret_cast<uint32_t*>(at + w.next) = code[1];
+  if ((w.word & 7) == 0) *reinterpret_cast<uint32_t*>(at + w.par(row)) = par;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kStoreThreads) kv4_append_kernel(const __grid_constant__ Kv4StoreParams p) {
+  __shared__ StorePlaces sp;
+  const long long token0 = static_cast<long long>(blockIdx.x) * p.block_tokens;
+  const int n = store_places<D>(p, token0, sp);
+  // every lane runs every loop (the shuffles need the whole warp)
+  const int total = 2 * p.heads * (D / 16), side = p.by_lanes(threadIdx.x);
+  for (int i0 = 0; i0 < total; i0 += p.lanes) {
+    const int i = i0 + static_cast<int>(threadIdx.x) - side * p.lanes;
+    const bool live = side < p.side_by_side && i < total;
+    const StoreWords<D> w(p, live ? i : 0);
+    const __nv_bfloat16* x = p.x[w.value] + w.h * p.sh[w.value] + w.word * 8;
+    for (int t = 0; t < n; t += kStoreBatch * p.side_by_side) {
+      uint32_t raw[kStoreBatch][8];
+      long long tile[kStoreBatch];
+#pragma unroll
+      for (int u = 0; u < kStoreBatch; ++u) {
+        const int tk = t + side + u * p.side_by_side;
+        tile[u] = live && tk < n ? sp.tile[tk] : -1;
+        uint4 a = make_uint4(0, 0, 0, 0), b = a;
+        if (tile[u] >= 0) {
+          const uint4* from = reinterpret_cast<const uint4*>(x + (token0 + tk) * p.st[w.value]);
+          a = __ldg(from);
+          b = __ldg(from + 1);
+        }
+        raw[u][0] = a.x, raw[u][1] = a.y, raw[u][2] = a.z, raw[u][3] = a.w;
+        raw[u][4] = b.x, raw[u][5] = b.y, raw[u][6] = b.z, raw[u][7] = b.w;
+      }
+#pragma unroll
+      for (int u = 0; u < kStoreBatch; ++u) {
+        if (t + u * p.side_by_side >= n) break;
+        append_words<D>(p, w, tile[u], tile[u] >= 0 ? sp.row[t + side + u * p.side_by_side] : 0, raw[u]);
+      }
+    }
   }
 }
 
@@ -175,35 +264,50 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const __grid_constant__
 // bits, so only its sum is rounded) and one rounding to bf16.  Slots outside
 // the cache give zeros.
 template <int D>
-__global__ void __launch_bounds__(256) kv4_gather_kernel(const __grid_constant__ Kv4StoreParams p) {
+__global__ void __launch_bounds__(kStoreThreads) kv4_gather_kernel(const __grid_constant__ Kv4StoreParams p) {
   using L = Kv4Tile<D>;
-  constexpr int kWords = D / 8;
-  const long long id = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (id >= p.n_items) return;
-  const int word = static_cast<int>(id % kWords);
-  const long long rest = id / kWords;
-  const int h = static_cast<int>(rest % p.heads);
-  const long long tk = rest / p.heads;
-  const int value = static_cast<int>(tk & 1);
-  const long long token = tk >> 1;
-  const long long slot = p.slots[token];
-  uint4 out = make_uint4(0, 0, 0, 0);
-  if (slot >= 0 && slot < p.n_slots) {
-    const uint8_t* tile = p.cache + kv4_tile_at<D>(p, slot, h);
-    const int row = static_cast<int>(slot & 15);
-    const uint32_t code = *reinterpret_cast<const uint32_t*>(
-        tile + (value ? L::kOffV : L::kOffK) + row * L::kRow + 4 * L::place(word, value != 0));
-    const uint32_t par = *reinterpret_cast<const uint32_t*>(
-        tile + (value ? L::kOffVPar : L::kOffKPar) + row * L::kPar + (word >> 3) * 4);
-    const float scale = bf16_lo(par), lo = bf16_hi(par);
-    float x[8];
+  __shared__ StorePlaces sp;
+  const long long token0 = static_cast<long long>(blockIdx.x) * p.block_tokens;
+  const int n = store_places<D>(p, token0, sp);
+  const int side = p.by_lanes(threadIdx.x);
+  if (side >= p.side_by_side) return;
+  for (int i = threadIdx.x - side * p.lanes; i < 2 * p.heads * (D / 16); i += p.lanes) {
+    const StoreWords<D> w(p, i);
+    __nv_bfloat16* y = p.y[w.value] + w.h * p.sh[w.value] + w.word * 8;
+    for (int t = side; t < n; t += kStoreBatch * p.side_by_side) {
+      uint32_t code[kStoreBatch][2] = {}, par[kStoreBatch] = {};
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      x[i] = fmaf(static_cast<float>((code >> (4 * i)) & 15u), scale, lo);
-    out = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                     pack_bf16x2(x[6], x[7]));
+      for (int u = 0; u < kStoreBatch; ++u) {
+        const int tk = t + u * p.side_by_side;
+        if (tk >= n || sp.tile[tk] < 0) continue;
+        const uint8_t* at = p.cache + sp.tile[tk] + w.in_cache + sp.row[tk] * L::kRow;
+        code[u][0] = __ldg(reinterpret_cast<const uint32_t*>(at));
+        code[u][1] = __ldg(reinterpret_cast<const uint32_t*>(at + w.next));
+        par[u] = __ldg(reinterpret_cast<const uint32_t*>(at + w.par(sp.row[tk])));
+      }
+#pragma unroll
+      for (int u = 0; u < kStoreBatch; ++u) {
+        const int tk = t + u * p.side_by_side;
+        if (tk >= n) continue;
+        const float scale = bf16_lo(par[u]), lo = bf16_hi(par[u]);
+        uint32_t out[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float x[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            // 2^23 + n, from n's bits
+            const uint32_t n_bits = (code[u][k >> 2] >> (8 * (k & 3) + 4 * e)) & 15u;
+            x[e] = fmaf(__uint_as_float(n_bits | 0x4b000000u) - 0x1p23f, scale, lo);
+          }
+          out[k] = pack_bf16x2(x[0], x[1]);
+        }
+        uint4* to = reinterpret_cast<uint4*>(y + (token0 + tk) * p.st[w.value]);
+        to[0] = make_uint4(out[0], out[1], out[2], out[3]);
+        to[1] = make_uint4(out[4], out[5], out[6], out[7]);
+      }
+    }
   }
-  *reinterpret_cast<uint4*>(p.y[value] + token * p.st[value] + h * p.sh[value] + word * 8) = out;
 }
 
 // ---------------------------------------------------------------- the plan

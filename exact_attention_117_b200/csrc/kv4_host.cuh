@@ -16,15 +16,6 @@ bool strides_multiple(const long long* s, int n, long long of) {
   return true;
 }
 
-template <typename T, int V>
-void launch_rotary(const fa::RotaryParams& p, bool interleaved, cudaStream_t st) {
-  const unsigned blocks = static_cast<unsigned>((p.n_threads + 255) / 256);
-  if (interleaved)
-    fa::rotary_kernel<T, V, true><<<blocks, 256, 0, st>>>(p);
-  else
-    fa::rotary_kernel<T, V, false><<<blocks, 256, 0, st>>>(p);
-}
-
 template <typename T>
 fa_status rotary_typed(fa::RotaryParams p, int B, bool interleaved, cudaStream_t st) {
   // Vectors of 16 bytes where the pairs, the channels behind them and every
@@ -40,24 +31,31 @@ fa_status rotary_typed(fa::RotaryParams p, int B, bool interleaved, cudaStream_t
   const int vec = wide ? kV : interleaved ? 2 : 1;
   const bool in_place = p.x[0] == p.y[0] && (!p.heads[1] || p.x[1] == p.y[1]);
   p.chunks = (interleaved ? p.rot : p.rot / 2) / vec + (in_place ? 0 : (p.d - p.rot) / vec);
-  const int heads = p.heads[0] + p.heads[1];
-  // Heads a thread walks: as many as leave about two threads for each of the
-  // GPU's slots, so that small calls spread out and large ones share sines.
-  const long long per = static_cast<long long>(B) * p.n * p.chunks;
-  int hpt = 16;
-  while (hpt > 1 && per * ((heads + hpt - 1) / hpt) < 2LL * 148 * 2048) hpt /= 2;
-  p.heads_per_thread = hpt;
-  p.groups = (heads + hpt - 1) / hpt;
-  p.n_threads = per * p.groups;
-  if (p.n_threads > (1LL << 38)) return FA_ERR_SHAPE;
+  // A block: up to 8 positions (512 sines, 256 vectors of a head), and as many
+  // heads as give each thread 8 vectors (so that sines are computed once for
+  // them) where that still fills the GPU, one otherwise.
+  const int heads = p.heads[0] + p.heads[1], pairs = p.rot / 2;
+  const long long all = static_cast<long long>(B) * p.n * heads * p.chunks;
+  const bool many = all >= 8LL * fa::kRotaryThreads * 148 * 3;
+  p.block_pos = std::max(1, std::min({many ? 8 : 1, fa::kRotaryPairs / pairs,
+                                      fa::kRotaryThreads / p.chunks, p.n}));
+  p.block_rows = p.block_pos * p.chunks;
+  p.block_heads = std::min(heads, (many ? 8 : 1) * (fa::kRotaryThreads / p.block_rows));
+  p.head_groups = (heads + p.block_heads - 1) / p.block_heads;
+  p.pos_blocks = (p.n + p.block_pos - 1) / p.block_pos;
+  const long long blocks = static_cast<long long>(B) * p.pos_blocks * p.head_groups;
+  if (blocks > 0x7fffffffLL) return FA_ERR_SHAPE;
+  const unsigned grid = static_cast<unsigned>(blocks);
   {
     LaunchTimer timer(st, FA_KERNEL_ROTARY);
-    if (wide)
-      launch_rotary<T, kV>(p, interleaved, st);
+    if (wide && interleaved)
+      fa::rotary_kernel<T, kV, true><<<grid, fa::kRotaryThreads, 0, st>>>(p);
+    else if (wide)
+      fa::rotary_kernel<T, kV, false><<<grid, fa::kRotaryThreads, 0, st>>>(p);
     else if (interleaved)
-      fa::rotary_kernel<T, 2, true><<<static_cast<unsigned>((p.n_threads + 255) / 256), 256, 0, st>>>(p);
+      fa::rotary_kernel<T, 2, true><<<grid, fa::kRotaryThreads, 0, st>>>(p);
     else
-      fa::rotary_kernel<T, 1, false><<<static_cast<unsigned>((p.n_threads + 255) / 256), 256, 0, st>>>(p);
+      fa::rotary_kernel<T, 1, false><<<grid, fa::kRotaryThreads, 0, st>>>(p);
   }
   return launched() ? FA_OK : FA_ERR_CUDA;
 }
@@ -73,8 +71,9 @@ fa_status store_params(fa::Kv4StoreParams* p, const void* k, const void* v, cons
   if (tokens < 0 || kv_heads < 1 || pages < 1 || page_size < 16 || page_size % 16)
     return FA_ERR_SHAPE;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED_D;
-  if (static_cast<long long>(pages) * page_size > (1LL << 40) / kv_heads ||
-      tokens > (1LL << 36) / kv_heads)
+  // tile numbers and the words of a block's tokens stay inside 31 bits
+  if (static_cast<long long>(pages) * page_size >= (1LL << 35) || kv_heads > (1 << 20) ||
+      tokens >= (1LL << 31))
     return FA_ERR_SHAPE;
   if (!aligned16(k) || !aligned16(v) || !aligned16(cache) ||
       (reinterpret_cast<uintptr_t>(slots) & 7u) || !strides_multiple(strides, 4, 8))
@@ -85,9 +84,17 @@ fa_status store_params(fa::Kv4StoreParams* p, const void* k, const void* v, cons
   p->sh[1] = strides[3];
   p->slots = slots;
   p->n_slots = static_cast<long long>(pages) * page_size;
-  p->n_items = tokens * kv_heads * 2 * (d / 8);
+  p->tokens = tokens;
   p->heads = kv_heads;
-  p->page_size = page_size;
+  p->page_tiles = page_size / 16;
+  p->by_page_tiles = fa::FastDiv::of(static_cast<uint32_t>(page_size / 16));
+  p->lanes = std::min(2 * kv_heads * (d / 16), fa::kStoreThreads);
+  p->side_by_side = fa::kStoreThreads / p->lanes;
+  p->by_lanes = fa::FastDiv::of(static_cast<uint32_t>(p->lanes));
+  // as many tokens a block as still leave every SM 8 blocks: 1 for a decode
+  // step, up to 16 for a prompt
+  p->block_tokens = static_cast<int>(
+      std::max<long long>(1, std::min<long long>(fa::kStoreTokens, tokens / (8LL * 148))));
   return FA_OK;
 }
 
@@ -257,12 +264,12 @@ fa_status fa_kv4_append(const void* k, const void* v, void* cache, const long lo
   p.x[1] = static_cast<const __nv_bfloat16*>(v);
   p.cache = static_cast<uint8_t*>(cache);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned blocks = static_cast<unsigned>((p.n_items + 255) / 256);
+  const unsigned blocks = static_cast<unsigned>((tokens + p.block_tokens - 1) / p.block_tokens);
   LaunchTimer timer(s, FA_KERNEL_KV4_APPEND);
   if (d == 64)
-    fa::kv4_append_kernel<64><<<blocks, 256, 0, s>>>(p);
+    fa::kv4_append_kernel<64><<<blocks, fa::kStoreThreads, 0, s>>>(p);
   else
-    fa::kv4_append_kernel<128><<<blocks, 256, 0, s>>>(p);
+    fa::kv4_append_kernel<128><<<blocks, fa::kStoreThreads, 0, s>>>(p);
   return launched() ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -276,12 +283,12 @@ fa_status fa_kv4_gather(const void* cache, const long long* slots, void* k, void
   p.y[1] = static_cast<__nv_bfloat16*>(v);
   p.cache = static_cast<uint8_t*>(const_cast<void*>(cache));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned blocks = static_cast<unsigned>((p.n_items + 255) / 256);
+  const unsigned blocks = static_cast<unsigned>((tokens + p.block_tokens - 1) / p.block_tokens);
   LaunchTimer timer(s, FA_KERNEL_KV4_GATHER);
   if (d == 64)
-    fa::kv4_gather_kernel<64><<<blocks, 256, 0, s>>>(p);
+    fa::kv4_gather_kernel<64><<<blocks, fa::kStoreThreads, 0, s>>>(p);
   else
-    fa::kv4_gather_kernel<128><<<blocks, 256, 0, s>>>(p);
+    fa::kv4_gather_kernel<128><<<blocks, fa::kStoreThreads, 0, s>>>(p);
   return launched() ? FA_OK : FA_ERR_CUDA;
 }
 
