@@ -566,6 +566,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, (Kv4AttendLayout<D, NT>::kCtas
   kv4_locate<L::kRows>(p, sh, cta, ctas);
   const Kv4Share share(sh.total, ctas);
   const long long u_begin = share.start(cta), u_end = share.start(cta + 1);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (u_begin >= u_end) return;
   int b = sh.found_b;
   long long excl = sh.found_excl;
@@ -789,10 +790,12 @@ __global__ void __launch_bounds__(kKv4Warps * 32, (Kv4AttendLayout<D, NT>::kCtas
   }
 }
 
-// Joins the partial results.  Block c looks at the start of CTA c + 1's range:
-// if it cuts a (request, row tile, head), and no earlier range start does, the
-// block owns that cut one and sums its pieces, left by the CTAs in order.  A
-// warp takes every fourth row; its lanes first find the pieces' weights.
+// Joins the partial results.  Block (c, y) looks at the start of CTA c + 1's
+// range: if it cuts a (request, row tile, head), and no earlier range start
+// does, the blocks of c own that cut one and sum its pieces, left by the CTAs
+// in order; each of their warps takes one row, its lanes first find the
+// pieces' weights.  It is launched while the attention kernel still runs, finds
+// its place meanwhile, and waits for that kernel's end before it reads.
 template <int D, int NT>
 __global__ void __launch_bounds__(kKv4Warps * 32)
     kv4_combine_kernel(const __grid_constant__ Kv4AttendParams p, int ctas) {
@@ -800,6 +803,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32)
   __shared__ Kv4Shared sh;
   const int cta = blockIdx.x + 1, lane = threadIdx.x & 31;
   kv4_locate<L::kRows>(p, sh, cta, ctas);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (sh.found_b < 0) return;
   const Kv4Share share(sh.total, ctas);
   const long long cut = share.start(cta);
@@ -807,49 +811,49 @@ __global__ void __launch_bounds__(kKv4Warps * 32)
   const long long job = kv4_div(cut - sh.found_excl, rq.chunks);
   const long long u0 = sh.found_excl + job * rq.chunks, u1 = u0 + rq.chunks;
   if (cut == u0 || share.start(cta - 1) > u0) return;
-  // CTAs first .. last hold a piece each (none is empty: it starts below u1)
-  const int first = cta - 1;
-  int last = cta;
-  while (share.start(last + 1) < u1) ++last;
   const int tile_row = static_cast<int>(kv4_div(job, p.kv_heads));
   const int h = static_cast<int>(job - static_cast<long long>(tile_row) * p.kv_heads);
   const int row0 = tile_row * L::kRows;
   const int rows = min(L::kRows, rq.n * p.group - row0);
+  const int r = blockIdx.y * kKv4Warps + (threadIdx.x >> 5);
+  if (r >= rows) return;
+  // CTAs first .. last hold a piece each (none is empty: it starts below u1)
+  const int first = cta - 1;
+  int last = cta;
+  while (share.start(last + 1) < u1) ++last;
   // piece k of the cut one: the first CTA left it in its second place if it
   // began there, all others in their first
   auto piece = [&](int k) {
     return p.part + (2LL * (first + k) + (k == 0 && share.start(first) <= u0 ? 1 : 0)) * L::kPartFloats;
   };
   const int n = last - first + 1;
-  for (int r = threadIdx.x >> 5; r < rows; r += kKv4Warps) {
-    float top = -INFINITY;
-    for (int k = lane; k < n; k += 32) top = fmaxf(top, piece(k)[L::kRows * D + r]);
+  float top = -INFINITY;
+  for (int k = lane; k < n; k += 32) top = fmaxf(top, piece(k)[L::kRows * D + r]);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float sum = 0.f, o[D / 32] = {};
-    for (int k0 = 0; k0 < n; k0 += 32) {
-      float w = 0.f;
-      if (k0 + lane < n) {
-        const float m = piece(k0 + lane)[L::kRows * D + r];
-        if (m != -INFINITY) {
-          w = ex2_approx(m - top);
-          sum = fmaf(piece(k0 + lane)[L::kRows * (D + 1) + r], w, sum);
-        }
-      }
-      const int here = min(32, n - k0);
-#pragma unroll 4
-      for (int k = 0; k < here; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, w, k);
-        float v[D / 32];
-        load_floats<D / 32>(piece(k0 + k) + r * D + lane * (D / 32), v);
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) o[c] = fmaf(v[c], wk, o[c]);
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float sum = 0.f, o[D / 32] = {};
+  for (int k0 = 0; k0 < n; k0 += 32) {
+    float w = 0.f;
+    if (k0 + lane < n) {
+      const float m = piece(k0 + lane)[L::kRows * D + r];
+      if (m != -INFINITY) {
+        w = ex2_approx(m - top);
+        sum = fmaf(piece(k0 + lane)[L::kRows * (D + 1) + r], w, sum);
       }
     }
+    const int here = min(32, n - k0);
+#pragma unroll 4
+    for (int k = 0; k < here; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      float v[D / 32];
+      load_floats<D / 32>(piece(k0 + k) + r * D + lane * (D / 32), v);
 #pragma unroll
-    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    kv4_store_row<D>(p, rq, h, row0 + r, lane, o, top, sum);
+      for (int c = 0; c < D / 32; ++c) o[c] = fmaf(v[c], wk, o[c]);
+    }
   }
+#pragma unroll
+  for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+  kv4_store_row<D>(p, rq, h, row0 + r, lane, o, top, sum);
 }
 
 }  // namespace fa

@@ -119,11 +119,19 @@ fa_status launch_attend(const fa::Kv4AttendParams& p, cudaStream_t st) {
     fa::kv4_attend_kernel<D, NT><<<ctas, fa::kKv4Warps * 32, L::kBytes, st>>>(p);
     if (!launched()) return FA_ERR_CUDA;
   }
-  {
-    LaunchTimer timer(st, FA_KERNEL_KV4_COMBINE);
-    fa::kv4_combine_kernel<D, NT><<<ctas - 1, fa::kKv4Warps * 32, 0, st>>>(p, ctas);
-  }
-  return launched() ? FA_OK : FA_ERR_CUDA;
+  LaunchTimer timer(st, FA_KERNEL_KV4_COMBINE);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas - 1), 2 * NT);
+  cfg.blockDim = dim3(fa::kKv4Warps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute early[1];
+  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fa::kv4_combine_kernel<D, NT>, p, ctas) == cudaSuccess && launched()
+             ? FA_OK
+             : FA_ERR_CUDA;
 }
 
 size_t attend_workspace(int d, int nt) {
