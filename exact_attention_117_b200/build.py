@@ -24,7 +24,7 @@ BINDING = os.path.join(PKG, "_fa_binding.so")  # Python extension module, host c
 DEBUG_LIB = os.path.join(PKG, "libfa_b200_debug.so")
 SOURCES = ["fa_api.cu"]
 HEADERS = ["sm100.cuh", "common.cuh", "fwd.cuh", "bwd.cuh", "bwd_main.cuh", "dq_pass.cuh", "kv_outer.cuh",
-           "rotary.cuh", "kv4.cuh", "kv4_attend.cuh", "kv4_host.cuh"]
+           "rotary.cuh", "kv4.cuh", "kv4_attend.cuh", "kv4_chunk.cuh", "kv4_host.cuh"]
 
 
 def nvcc() -> str:

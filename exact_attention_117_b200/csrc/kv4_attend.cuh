@@ -53,26 +53,39 @@ constexpr int kKv4Warps = 4;
 constexpr int kKv4Chunk = 32 * kKv4Warps;  // keys of a work unit
 
 // ------------------------------------------------------------ the work's order
-// Units: (request, row tile, kv head, chunk of keys), chunks innermost.  Each CTA
-// takes an equal, contiguous range of them, and so reads the same share of the
-// cache whatever the lengths are.  A (request, row tile, head) that a
-// CTA's range cuts is left as partial results, which the combine kernel joins.
+// Units: (request, tile of ROWS rows, kv head, UNIT keys), keys innermost; a row
+// tile has as many as its last row's visible keys fill (one if it sees none, so
+// that its zeros are written).  Each CTA takes an equal, contiguous range of
+// them, and so reads the same share of the cache whatever the lengths are.  A
+// (request, row tile, head) that a CTA's range cuts is left as partial results,
+// which the combine kernel joins.
 struct Kv4Req {
-  int first, n, len, row_tiles, chunks;
+  int first, n, len, rows;  // first query, queries, keys, rows (queries * group)
 };
-template <int ROWS>  // rows of a tile
 __device__ __forceinline__ Kv4Req kv4_request(const Kv4AttendParams& p, int b) {
   Kv4Req r;
   r.first = min(max(p.cu_tokens[b], 0), p.tokens);
   r.n = max(min(p.cu_tokens[b + 1], p.tokens) - r.first, 0);
   r.len = max(0, static_cast<int>(min(static_cast<long long>(p.lengths[b]),
                                       static_cast<long long>(p.width) * p.page_size)));
-  r.row_tiles = static_cast<int>((static_cast<long long>(r.n) * p.group + ROWS - 1) / ROWS);
-  r.chunks = max(1, (r.len + kKv4Chunk - 1) / kKv4Chunk);
+  r.rows = r.n * p.group;
   return r;
 }
+// Keys that row `row` of a request sees.
+__device__ __forceinline__ int kv4_sees(const Kv4AttendParams& p, const Kv4Req& r, int row) {
+  return p.causal ? min(max(r.len - r.n + static_cast<int>(p.by_group(row)) + 1, 0), r.len) : r.len;
+}
+// Units of a row tile for one head.
+template <int ROWS, int UNIT>
+__device__ __forceinline__ int kv4_tile_units(const Kv4AttendParams& p, const Kv4Req& r, int tile) {
+  const int last = min((tile + 1) * ROWS, r.rows) - 1;
+  return max(1, (kv4_sees(p, r, last) + UNIT - 1) / UNIT);
+}
+template <int ROWS, int UNIT>
 __device__ __forceinline__ long long kv4_units(const Kv4AttendParams& p, const Kv4Req& r) {
-  return static_cast<long long>(r.row_tiles) * p.kv_heads * r.chunks;
+  long long sum = 0;
+  for (int t = 0; t * ROWS < r.rows; ++t) sum += kv4_tile_units<ROWS, UNIT>(p, r, t);
+  return sum * p.kv_heads;
 }
 
 // a / b for non-negative numbers, in 32 bits where they fit (nearly always).
@@ -93,19 +106,20 @@ struct Kv4Share {  // of the units: CTA c of n starts at each * c + min(c, rest)
 };
 
 struct Kv4Shared {
-  long long warp_sum[kKv4Warps];
+  long long warp_sum[32];
   long long total, found_excl;
   int found_b;
 };
 
-// Block-wide: the total number of units, and the request that holds the first
-// unit of CTA `cta` of `ctas` together with the units before it (-1 if there is
-// none).  Up to 128 requests are summed once, more are walked twice.
-template <int ROWS>
+// Block-wide (kWarps warps): the total number of units, and the request that
+// holds the first unit of CTA `cta` of `ctas` together with the units before it
+// (-1 if there is none).  Requests up to the number of threads are summed once,
+// more are walked twice.
+template <int ROWS, int UNIT, int kWarps>
 __device__ __forceinline__ void kv4_locate(const Kv4AttendParams& p, Kv4Shared& sh, int cta,
                                            int ctas) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kThreads = kKv4Warps * 32;
+  constexpr int kThreads = kWarps * 32;
   const int chunks = (p.requests + kThreads - 1) / kThreads;
   long long total = 0, mine = 0, incl = 0;
   if (tid == 0) sh.found_b = -1;
@@ -114,7 +128,7 @@ __device__ __forceinline__ void kv4_locate(const Kv4AttendParams& p, Kv4Shared& 
     for (int c = 0; c < chunks; ++c) {
       const int b = c * kThreads + tid;
       if (pass == 0 || chunks > 1) {
-        mine = b < p.requests ? kv4_units(p, kv4_request<ROWS>(p, b)) : 0;
+        mine = b < p.requests ? kv4_units<ROWS, UNIT>(p, kv4_request(p, b)) : 0;
         incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -126,7 +140,7 @@ __device__ __forceinline__ void kv4_locate(const Kv4AttendParams& p, Kv4Shared& 
         __syncthreads();
         long long all = 0;
 #pragma unroll
-        for (int w = 0; w < kKv4Warps; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
           if (w < warp) incl += sh.warp_sum[w];
           all += sh.warp_sum[w];
         }
@@ -146,6 +160,36 @@ __device__ __forceinline__ void kv4_locate(const Kv4AttendParams& p, Kv4Shared& 
   if (tid == 0) sh.total = total;
   __syncthreads();
 }
+
+// Where unit u lies, walked forwards from the start of a request.
+template <int ROWS, int UNIT>
+struct Kv4Walk {
+  int b, tile, units;  // request, row tile, units of the tile for one head
+  long long excl;      // units before the tile
+  Kv4Req rq;
+  int h, c0;           // of unit u: kv head, unit inside (tile, head)
+  __device__ __forceinline__ Kv4Walk(const Kv4AttendParams& p, int b_, long long excl_)
+      : b(b_), tile(0), excl(excl_), rq(kv4_request(p, b_)) {
+    units = kv4_tile_units<ROWS, UNIT>(p, rq, 0);
+  }
+  // u at or behind the last one, and inside the work
+  __device__ __forceinline__ void to(const Kv4AttendParams& p, long long u) {
+    while (u - excl >= static_cast<long long>(units) * p.kv_heads) {
+      excl += static_cast<long long>(units) * p.kv_heads;
+      if (++tile * ROWS >= rq.rows) {
+        do rq = kv4_request(p, ++b);
+        while (rq.rows == 0);
+        tile = 0;
+      }
+      units = kv4_tile_units<ROWS, UNIT>(p, rq, tile);
+    }
+    h = static_cast<int>(kv4_div(u - excl, units));
+    c0 = static_cast<int>(u - excl - static_cast<long long>(h) * units);
+  }
+  __device__ __forceinline__ long long job_start() const {
+    return excl + static_cast<long long>(h) * units;
+  }
+};
 
 // ------------------------------------------------------------ matrix pieces
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -563,34 +607,23 @@ __global__ void __launch_bounds__(kKv4Warps * 32, (Kv4AttendLayout<D, NT>::kCtas
   if (tid == 0) abort_word = 0;
   fence_barrier_init();
   fence_proxy_async_smem();
-  kv4_locate<L::kRows>(p, sh, cta, ctas);
+  kv4_locate<L::kRows, kKv4Chunk, kKv4Warps>(p, sh, cta, ctas);
   const Kv4Share share(sh.total, ctas);
   const long long u_begin = share.start(cta), u_end = share.start(cta + 1);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (u_begin >= u_end) return;
-  int b = sh.found_b;
-  long long excl = sh.found_excl;
-  Kv4Req rq = kv4_request<L::kRows>(p, b);
+  Kv4Walk<L::kRows, kKv4Chunk> walk(p, sh.found_b, sh.found_excl);
   const int tiles_per_page = p.page_size / 16;
   int it = 0;  // blocks this warp has taken from its ring
 
   for (long long u = u_begin; u < u_end;) {
-    while (u - excl >= kv4_units(p, rq)) {
-      excl += kv4_units(p, rq);
-      rq = kv4_request<L::kRows>(p, ++b);
-    }
-    const long long job = kv4_div(u - excl, rq.chunks);
-    const int c0 = static_cast<int>(u - excl - job * rq.chunks);
-    const int c1 = static_cast<int>(min(static_cast<long long>(rq.chunks), c0 + (u_end - u)));
-    const int tile_row = static_cast<int>(kv4_div(job, p.kv_heads));
-    const int h = static_cast<int>(job - static_cast<long long>(tile_row) * p.kv_heads);
-    const int row0 = tile_row * L::kRows;
-    const int rows = min(L::kRows, rq.n * p.group - row0);
-    // keys that query token i of the request sees
-    auto sees = [&](int i) {
-      return p.causal ? min(max(rq.len - rq.n + i + 1, 0), rq.len) : rq.len;
-    };
-    const int all_see = sees(p.by_group(row0)), any_sees = sees(p.by_group(row0 + rows - 1));
+    walk.to(p, u);
+    const Kv4Req& rq = walk.rq;
+    const int b = walk.b, h = walk.h, c0 = walk.c0;
+    const int c1 = static_cast<int>(min(static_cast<long long>(walk.units), c0 + (u_end - u)));
+    const int row0 = walk.tile * L::kRows;
+    const int rows = min(L::kRows, rq.rows - row0);
+    const int all_see = kv4_sees(p, rq, row0), any_sees = kv4_sees(p, rq, row0 + rows - 1);
 
     // ---- fill the ring; pages of the block after next are looked up an
     // iteration ahead of their copy
@@ -668,7 +701,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, (Kv4AttendLayout<D, NT>::kCtas
           qs[nt][gp][i] = NT > 2 ? s_qs[(nt * kGroups + gp) * 8 + 2 * t + i]
                                  : __shfl_sync(0xffffffffu, sum[gp], (2 * t + i) * 4);
         rs[nt][i] = NT > 2 ? s_rs[r] : __shfl_sync(0xffffffffu, factor, (2 * t + i) * 4);
-        lim[nt][i] = r < rows ? sees(p.by_group(row0 + r)) : 0;
+        lim[nt][i] = r < rows ? kv4_sees(p, rq, row0 + r) : 0;
       }
     }
 
@@ -756,7 +789,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, (Kv4AttendLayout<D, NT>::kCtas
       }
     __syncthreads();
     // a warp takes every fourth row: a lane D / 32 channels
-    const bool whole = c0 == 0 && c1 == rq.chunks;
+    const bool whole = c0 == 0 && c1 == walk.units;
     float* part = p.part + (2LL * cta + (u == u_begin && c0 > 0 ? 0 : 1)) * L::kPartFloats;
     for (int r = warp; r < rows; r += kKv4Warps) {
       float top = -INFINITY, sum = 0.f, f[kKv4Warps], o[D / 32] = {};
@@ -802,19 +835,18 @@ __global__ void __launch_bounds__(kKv4Warps * 32)
   using L = Kv4AttendLayout<D, NT>;
   __shared__ Kv4Shared sh;
   const int cta = blockIdx.x + 1, lane = threadIdx.x & 31;
-  kv4_locate<L::kRows>(p, sh, cta, ctas);
+  kv4_locate<L::kRows, kKv4Chunk, kKv4Warps>(p, sh, cta, ctas);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (sh.found_b < 0) return;
   const Kv4Share share(sh.total, ctas);
   const long long cut = share.start(cta);
-  const Kv4Req rq = kv4_request<L::kRows>(p, sh.found_b);
-  const long long job = kv4_div(cut - sh.found_excl, rq.chunks);
-  const long long u0 = sh.found_excl + job * rq.chunks, u1 = u0 + rq.chunks;
+  Kv4Walk<L::kRows, kKv4Chunk> walk(p, sh.found_b, sh.found_excl);
+  walk.to(p, cut);
+  const Kv4Req& rq = walk.rq;
+  const long long u0 = walk.job_start(), u1 = u0 + walk.units;
   if (cut == u0 || share.start(cta - 1) > u0) return;
-  const int tile_row = static_cast<int>(kv4_div(job, p.kv_heads));
-  const int h = static_cast<int>(job - static_cast<long long>(tile_row) * p.kv_heads);
-  const int row0 = tile_row * L::kRows;
-  const int rows = min(L::kRows, rq.n * p.group - row0);
+  const int h = walk.h, row0 = walk.tile * L::kRows;
+  const int rows = min(L::kRows, rq.rows - row0);
   const int r = blockIdx.y * kKv4Warps + (threadIdx.x >> 5);
   if (r >= rows) return;
   // CTAs first .. last hold a piece each (none is empty: it starts below u1)

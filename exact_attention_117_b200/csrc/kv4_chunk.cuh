@@ -1,0 +1,673 @@
+// kv4_chunk.cuh -- attention over the paged 4-bit cache for many query rows (a
+// prompt's chunk, long drafts): the tcgen05 form of kv4_attend.cuh.
+//
+// Same operation, layouts and order of work; here a work item is 256 rows (two
+// tiles of 128; row = query * group + head) of one request and kv head against
+// 128-key tiles, with S = Q K^T and O += P V on tcgen05 (fp16 operands, fp32
+// accumulators in TMEM).
+//
+// Operands.  Q rows enter as fp16 times a power of two that brings the row's
+// largest element near fp16's largest (exact for bf16 and fp16 input down to
+// 2^-24 of it).  K and V tiles are put together by four warps from the codes:
+// lowest + scale n in one fused multiply-add, rounded once to fp16, in units of
+// a power of two that is the tile's for K and the largest so far for V (O is
+// rescaled when it grows).  So a key or value is off by 2^-12 of itself, an
+// eighth of what a bf16 copy of the cache would be off, and the scores by
+// about 2^-12 of their terms' root mean square; P is fp16 as in kv4_attend.cuh,
+// statistics and O are fp32.  The channels of a 64-bit chunk of codes stay in
+// the order in which they come out of a word, (0, 4), (1, 5), (2, 6), (3, 7):
+// Q is laid out alike, and O's columns are put back in order when they leave.
+//
+// Warps (512 threads, one CTA an SM): 0 issues the MMAs; 4-7 put K and V
+// together (one key a thread, the next tile's codes already in registers);
+// 8-11 and 12-15 lay out the rows of Q tile 0 and 1, run their softmax (one
+// row a thread, the exponentials against the running maximum, the tile redone
+// only where a score passes it by 2^14) and write O.
+//
+// Bound: the tensor cores and the softmax, as the forward kernel; the codes are
+// read once an item, an eighth of the bytes of a bf16 cache.
+#pragma once
+
+#include "kv4_attend.cuh"
+
+namespace fa {
+
+constexpr int kChunkRows = 256;
+constexpr int kChunkUnit = 256;  // keys of a work unit
+constexpr int kChunkWarps = 16;
+
+template <int D>
+struct Kv4ChunkLayout {
+  static constexpr int kTile = 128 * D * 2;  // bytes of a Q, K or V tile
+  static constexpr int kStages = 2;
+  static constexpr int kOffQ = 0;            // two tiles
+  static constexpr int kOffK = 2 * kTile;
+  static constexpr int kOffV = kOffK + kStages * kTile;
+  static constexpr int kOffBar = kOffV + kStages * kTile;
+  static constexpr int kQFull = 0;                  // [2] row tile laid out
+  static constexpr int kKFull = 2;                  // [stages]
+  static constexpr int kKEmpty = kKFull + kStages;
+  static constexpr int kVFull = kKEmpty + kStages;
+  static constexpr int kVEmpty = kVFull + kStages;
+  static constexpr int kSFull = kVEmpty + kStages;  // [2]
+  static constexpr int kPFull = kSFull + 2;         // [2]
+  static constexpr int kOFinal = kPFull + 2;        // [2]
+  static constexpr int kSize = kOFinal + 2;         // the tile's powers of two are known
+  static constexpr int kDrain = kSize + 1;
+  static constexpr int kNumBars = kDrain + 1;
+  static constexpr int kOffSlot = kOffBar + 8 * kNumBars;  // TMEM base address
+  static constexpr int kOffAbort = kOffSlot + 4;
+  static constexpr int kBytes = kOffAbort + 8;
+  static constexpr int kSmemAlloc = kBytes + 1024;  // slack to align the base to 1 KiB
+  static_assert(kSmemAlloc + 1024 <= 232448, "shared memory budget");
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kColS = 0, kColO = 256;  // S: 128 columns a tile, O: D
+  static constexpr int kPartFloats = kChunkRows * (D + 2);
+  static constexpr uint32_t kRegsOther = 64, kRegsPut = 96, kRegsSoftmax = 176;
+  static_assert(128 * (kRegsOther + kRegsPut + 2 * kRegsSoftmax) <= 512 * 128, "register split");
+};
+
+// fp16 A and B, fp32 D (see idesc_bf16_f32; format 0 is fp16).
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// One cut of the work: `tiles[t]` key tiles of row tile t from key tile k0 on.
+struct ChunkPiece {
+  int b, h, row0, rows, k0, tiles[2], most;
+  bool whole, head_cut;  // all of the (tile, head); begun by an earlier CTA
+};
+__device__ __forceinline__ ChunkPiece chunk_piece(const Kv4AttendParams& p,
+                                                  const Kv4Walk<kChunkRows, kChunkUnit>& w,
+                                                  int units) {
+  ChunkPiece c;
+  c.b = w.b;
+  c.h = w.h;
+  c.row0 = w.tile * kChunkRows;
+  c.rows = min(kChunkRows, w.rq.rows - c.row0);
+  c.k0 = w.c0 * (kChunkUnit / 128);
+  c.whole = w.c0 == 0 && units == w.units;
+  c.head_cut = w.c0 > 0;
+  const int end = c.k0 + units * (kChunkUnit / 128);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int last = min(128 * (t + 1), c.rows) - 1;
+    const int see = last >= 128 * t ? kv4_sees(p, w.rq, c.row0 + last) : 0;
+    c.tiles[t] = max(0, min(end, (see + 127) / 128) - c.k0);
+  }
+  c.most = max(c.tiles[0], c.tiles[1]);
+  return c;
+}
+
+// 8 codes as fp16 lowest + scale n, pairs (0, 4), (1, 5), (2, 6), (3, 7).  The
+// codes are subnormal numbers n 2^-24 or 16 n 2^-24; s24 and s20 carry 2^24 and
+// 2^20 times the scale.
+__device__ __forceinline__ uint4 put_word(uint32_t w, uint32_t s24, uint32_t s20, uint32_t lo) {
+  uint32_t c[4], r[4];
+  codes_f16(w, c);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r[i]) : "r"(c[i]), "r"(i & 1 ? s20 : s24), "r"(lo));
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// Shared memory of a CTA beside the tiles: what a key tile's factors are, by
+// tile number mod 4 (the softmax is at most two tiles behind).
+struct ChunkShared {
+  float k_up[4];          // K in the tile is K / k_up
+  float v_up[4];          // V likewise, never smaller than before in a piece
+  alignas(16) uint32_t absent[4][4];  // keys whose page lies outside the cache
+  int size[2][4][2];      // per warp: largest exponent of K and V, by tile parity
+};
+
+template <int D>
+__global__ void __launch_bounds__(kChunkWarps * 32, 1)
+    kv4_chunk_kernel(const __grid_constant__ Kv4AttendParams p) {
+  using L = Kv4ChunkLayout<D>;
+  using T = Kv4Tile<D>;
+  constexpr int S = L::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Kv4Shared sh;
+  __shared__ ChunkShared cs;
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  const uint32_t sb = smem_u32(smem);
+  auto bar = [&](int i) -> uint32_t { return sb + L::kOffBar + 8u * static_cast<uint32_t>(i); };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffAbort);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffSlot);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ctas = gridDim.x, cta = blockIdx.x;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kNumBars; ++i) {
+      // four warps lay out a tile, put K and V together, write P, find sizes
+      const bool by_warps = i < L::kKEmpty || (i >= L::kVFull && i < L::kVEmpty) ||
+                            (i >= L::kPFull && i < L::kPFull + 2) || i == L::kSize;
+      mbar_init(bar(i), by_warps ? 4 : 1);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  kv4_locate<kChunkRows, kChunkUnit, kChunkWarps>(p, sh, cta, ctas);  // (a block barrier)
+  tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t tmem = *tmem_slot;
+  const Kv4Share share(sh.total, ctas);
+  const long long u_begin = share.start(cta), u_end = share.start(cta + 1);
+  const bool any = u_begin < u_end;
+  const uint64_t limit = p.limit_ns;
+
+  if (warp < 4) {
+    setmaxnreg_dec<L::kRegsOther>();
+    if (warp == 0 && any) {
+      // ------------------------------------------------------------ MMA issuer
+      constexpr uint32_t id_s = idesc_f16_f32(128, 128, false);
+      constexpr uint32_t id_o = idesc_f16_f32(128, D, true);
+      constexpr unsigned int err = kErrKv4 | kErrRoleMma;
+      auto issue_s = [&](int t, int g) {  // S_t = Q_t K^T, K from ring position g
+        const uint32_t qa = sb + L::kOffQ + t * L::kTile, ka = sb + L::kOffK + (g % S) * L::kTile;
+#pragma unroll 2
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+          mma_bf16_ss(tmem + L::kColS + t * 128, sw128_desc(qa + off, 16, 1024),
+                      sw128_desc(ka + off, 16, 1024), id_s, kk > 0 ? 1u : 0u);
+        }
+        tc_commit(bar(L::kSFull + t));
+      };
+      auto issue_pv = [&](int t, int g, bool first) {  // O_t (+)= P_t V
+        const uint32_t va = sb + L::kOffV + (g % S) * L::kTile;
+#pragma unroll 2
+        for (int kk = 0; kk < 8; ++kk)
+          mma_bf16_ts(tmem + L::kColO + t * D, tmem + L::kColS + t * 128 + kk * 8,
+                      sw128_desc(va + kk * 2048, 16384, 1024), id_o, (!first || kk > 0) ? 1u : 0u);
+      };
+      Kv4Walk<kChunkRows, kChunkUnit> walk(p, sh.found_b, sh.found_excl);
+      int g = 0, pieces[2] = {0, 0}, steps[2] = {0, 0};  // key tiles, Q tiles, P tiles so far
+      bool ok = true;
+      for (long long u = u_begin; u < u_end && ok;) {
+        walk.to(p, u);
+        const int units = static_cast<int>(min(static_cast<long long>(walk.units - walk.c0), u_end - u));
+        const ChunkPiece c = chunk_piece(p, walk, units);
+        u += units;
+        if (c.most == 0) continue;
+        for (int t = 0; t < 2 && ok; ++t)
+          if (c.tiles[t] > 0) {
+            ok = wait_bounded_warp(bar(L::kQFull + t), pieces[t] & 1, limit, abort_flag, err);
+            ++pieces[t];
+          }
+        ok = ok && wait_bounded_warp(bar(L::kKFull + g % S), (g / S) & 1, limit, abort_flag, err);
+        if (!ok) break;
+        tc_fence_after();
+        for (int t = 0; t < 2; ++t)
+          if (c.tiles[t] > 0) issue_s(t, g);
+        tc_commit(bar(L::kKEmpty + g % S));
+        for (int j = 0; j < c.most && ok; ++j, ++g) {
+          const int s = g % S, s1 = (g + 1) % S;
+          ok = wait_bounded_warp(bar(L::kVFull + s), (g / S) & 1, limit, abort_flag, err);
+          bool k_seen = false;
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (j >= c.tiles[t]) continue;
+            ok = wait_bounded_warp(bar(L::kPFull + t), steps[t] & 1, limit, abort_flag, err);
+            if (!ok) break;
+            ++steps[t];
+            tc_fence_after();
+            issue_pv(t, g, j == 0);
+            if (j + 1 == c.tiles[t]) {
+              tc_commit(bar(L::kOFinal + t));
+            } else {
+              if (!k_seen)
+                ok = wait_bounded_warp(bar(L::kKFull + s1), ((g + 1) / S) & 1, limit, abort_flag, err);
+              k_seen = true;
+              if (!ok) break;
+              tc_fence_after();
+              issue_s(t, g + 1);
+            }
+          }
+          if (!ok) break;
+          tc_commit(bar(L::kVEmpty + s));
+          if (j + 1 < c.most) tc_commit(bar(L::kKEmpty + s1));
+        }
+      }
+      // every MMA issued above must finish before TMEM / smem are released
+      tc_commit(bar(L::kDrain));
+      drain_wait(bar(L::kDrain), 0, limit);
+      __syncwarp();
+    }
+  } else if (warp < 8) {
+    setmaxnreg_dec<L::kRegsPut>();
+    if (any) {
+      // ------------------------------------------- K and V from their codes
+      constexpr unsigned int err = kErrKv4 | kErrRoleLoad;
+      const int row = threadIdx.x - 128;  // the thread's key of each tile
+      const int tiles_per_page = p.page_size / 16;
+      const long long page_bytes = static_cast<long long>(p.kv_heads) * tiles_per_page * T::kBytes;
+      // raw codes of one key; `there`: 0 no such key, 1 a key, 2 its page is
+      // outside the cache
+      uint32_t kc[D / 8], vc[D / 8], kp[D / 64], vp[D / 64];
+      int there = 0;
+      // Keys from `sure` on are hidden from some rows: 0 times a value that
+      // is no finite number would reach them, so there a key that has one gets
+      // values 0 and a score of NaN instead, for the rows that see it.
+      auto fetch = [&](const ChunkPiece& c, int len, int sure, int j) {
+        const int key = (c.k0 + j) * 128 + row;
+        there = key < len ? 1 : 0;
+        if (there) {
+          const int tile = key >> 4, page = p.page_tiles(tile), id = p.table[c.b * p.table_stride + page];
+          if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.pages)) {
+            there = 2;
+            atomicOr(&g_error_word, kErrBadPage);
+          } else {
+            const uint8_t* at = p.cache + id * page_bytes +
+                                (static_cast<long long>(c.h) * tiles_per_page + tile - page * tiles_per_page) * T::kBytes;
+            const uint8_t* k = at + T::kOffK + (key & 15) * T::kRow;
+            const uint8_t* v = at + T::kOffV + (key & 15) * T::kRow;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+              load_words<4>(k + 16 * i, *reinterpret_cast<uint32_t(*)[4]>(&kc[4 * i]));
+              load_words<4>(v + 16 * i, *reinterpret_cast<uint32_t(*)[4]>(&vc[4 * i]));
+            }
+            load_words<D / 64>(at + T::kOffKPar + (key & 15) * T::kPar, kp);
+            load_words<D / 64>(at + T::kOffVPar + (key & 15) * T::kPar, vp);
+            bool odd = false;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) odd |= !isfinite(bf16_hi(vp[i])) || !isfinite(bf16_lo(vp[i]));
+            if (odd && key >= sure) {
+#pragma unroll
+              for (int i = 0; i < D / 64; ++i) {
+                vp[i] = 0;
+                kp[i] = 0x7fc00000u;
+              }
+            }
+          }
+        }
+        if (there != 1) {
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i) kp[i] = vp[i] = 0;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) kc[i] = vc[i] = 0;
+        }
+      };
+      // exponent of the largest value a pair of parameters stands for
+      auto size_of = [&](const uint32_t (&par)[D / 64]) {
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          const float s = bf16_lo(par[i]), lo = bf16_hi(par[i]);
+          top = fmaxf(top, fmaxf(fabsf(lo), fabsf(fmaf(15.f, s, lo))));
+        }
+        return min(static_cast<int>(__float_as_uint(top) >> 23), 254);
+      };
+      const uint32_t to_row = row * 128;
+      // a key's row of a tile: chunk w of 8 channels is word w's
+      auto put = [&](uint32_t base, const uint32_t (&code)[D / 8], const uint32_t (&par)[D / 64],
+                     float unit, bool value) {
+        uint32_t s24[D / 64], s20[D / 64], lo[D / 64];
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          const float s = bf16_lo(par[i]) * unit, l = bf16_hi(par[i]) * unit;
+          s24[i] = pack_f16x2(s * 0x1p24f, s * 0x1p24f);
+          s20[i] = pack_f16x2(s * 0x1p20f, s * 0x1p20f);
+          lo[i] = pack_f16x2(l, l);
+        }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {  // place i of the row
+          const int w = value ? 8 * (i % (D / 64)) + i / (D / 64) : 4 * (i % (D / 32)) + i / (D / 32);
+          const uint4 x = put_word(code[i], s24[w >> 3], s20[w >> 3], lo[w >> 3]);
+          st_shared_v4(base + (w >> 3) * 16384 + to_row + (((w & 7) ^ (row & 7)) << 4), x.x, x.y,
+                       x.z, x.w);
+        }
+      };
+      Kv4Walk<kChunkRows, kChunkUnit> walk(p, sh.found_b, sh.found_excl);
+      int g = 0;  // key tiles so far
+      bool ok = true;
+      for (long long u = u_begin; u < u_end && ok;) {
+        walk.to(p, u);
+        const int units = static_cast<int>(min(static_cast<long long>(walk.units - walk.c0), u_end - u));
+        const ChunkPiece c = chunk_piece(p, walk, units);
+        u += units;
+        int v_size = 0;  // exponent of V's unit so far in this piece
+        const int sure = kv4_sees(p, walk.rq, c.row0);
+        if (c.most > 0) fetch(c, walk.rq.len, sure, 0);
+        for (int j = 0; j < c.most; ++j, ++g) {
+          const int s = g % S;
+          // the tile's sizes, over the four warps
+          const int ek = __reduce_max_sync(0xffffffffu, size_of(kp));
+          const int ev = __reduce_max_sync(0xffffffffu, size_of(vp));
+          const uint32_t gone = __ballot_sync(0xffffffffu, there == 2);
+          if (lane == 0) {
+            cs.size[g & 1][warp - 4][0] = ek;
+            cs.size[g & 1][warp - 4][1] = ev;
+            cs.absent[g & 3][warp - 4] = gone;
+            mbar_arrive(bar(L::kSize));
+          }
+          if (!(ok = wait_bounded_warp(bar(L::kSize), g & 1, limit, abort_flag, err))) break;
+          int k_size = 0;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            k_size = max(k_size, cs.size[g & 1][w][0]);
+            v_size = max(v_size, cs.size[g & 1][w][1]);
+          }
+          // the largest value to [2^-8, 2^-7): scale 2^24 stays below fp16's
+          // largest (exponents kept where both powers are normal numbers: values
+          // from 2^119 on come out infinite)
+          const int xk = min(max(k_size, 20), 245), xv = min(max(v_size, 20), 245);
+          const float k_unit = __uint_as_float(static_cast<uint32_t>(246 - xk) << 23);
+          const float v_unit = __uint_as_float(static_cast<uint32_t>(246 - xv) << 23);
+          if (threadIdx.x == 128) {
+            cs.k_up[g & 3] = __uint_as_float(static_cast<uint32_t>(xk + 8) << 23);
+            cs.v_up[g & 3] = __uint_as_float(static_cast<uint32_t>(xv + 8) << 23);
+          }
+          if (!(ok = wait_bounded_warp(bar(L::kKEmpty + s), ((g / S) & 1) ^ 1, limit, abort_flag, err)))
+            break;
+          put(sb + L::kOffK + s * L::kTile, kc, kp, k_unit, false);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::kKFull + s));
+          if (!(ok = wait_bounded_warp(bar(L::kVEmpty + s), ((g / S) & 1) ^ 1, limit, abort_flag, err)))
+            break;
+          put(sb + L::kOffV + s * L::kTile, vc, vp, v_unit, true);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::kVFull + s));
+          if (j + 1 < c.most) fetch(c, walk.rq.len, sure, j + 1);
+        }
+      }
+    }
+  } else {
+    setmaxnreg_inc<L::kRegsSoftmax>();
+    if (any) {
+      // --------------------------------------------------- rows, softmax, output
+      constexpr unsigned int err = kErrKv4 | kErrRoleSoftmax;
+      const int t = warp >= 12 ? 1 : 0;
+      const int r = threadIdx.x - 256 - 128 * t;  // row of the tile == TMEM lane
+      const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t s_addr = tmem + lane_off + L::kColS + t * 128;
+      const uint32_t o_addr = tmem + lane_off + L::kColO + t * D;
+      Kv4Walk<kChunkRows, kChunkUnit> walk(p, sh.found_b, sh.found_excl);
+      int g = 0, steps = 0, finals = 0;  // key tiles of the CTA, of this row tile; outputs
+      bool ok = true;
+      for (long long u = u_begin; u < u_end && ok;) {
+        walk.to(p, u);
+        const int units = static_cast<int>(min(static_cast<long long>(walk.units - walk.c0), u_end - u));
+        const ChunkPiece c = chunk_piece(p, walk, units);
+        float* part = p.part + (2LL * cta + (u == u_begin && c.head_cut ? 0 : 1)) * L::kPartFloats;
+        u += units;
+        const Kv4Req rq = walk.rq;
+        const int in_tile = 128 * t + r, row = c.row0 + in_tile;
+        const bool real = in_tile < c.rows;
+        const int tok = p.by_group(row), head = c.h * p.group + row - tok * p.group;
+        const int n = c.tiles[t];
+        float factor = 0.f;  // from scores in the tile's units to base-2 exponents
+        if (n > 0) {
+          // ---- this row of Q: fp16 times a power of two, in the channel order
+          // of the codes' pairs; a negative scale is taken into Q
+          uint32_t raw[D / 2];
+          float top = 0.f;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (real)
+              x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
+                                                  (rq.first + tok) * p.q_st + head * p.q_sh + 8 * i);
+            raw[4 * i] = x.x, raw[4 * i + 1] = x.y, raw[4 * i + 2] = x.z, raw[4 * i + 3] = x.w;
+          }
+          auto pair = [&](int i) {
+            return p.is_half ? __half22float2(*reinterpret_cast<const __half2*>(&raw[i]))
+                             : make_float2(bf16_lo(raw[i]), bf16_hi(raw[i]));
+          };
+#pragma unroll
+          for (int i = 0; i < D / 2; ++i) {
+            const float2 v = pair(i);
+            top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+          }
+          const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23), 27), 227);
+          float down = __uint_as_float(static_cast<uint32_t>(254 + 14 - e) << 23);
+          factor = __uint_as_float(static_cast<uint32_t>(e - 14) << 23) * fabsf(p.scale_log2);
+          if (p.scale_log2 < 0.f) down = -down;
+          const uint32_t q_row = sb + L::kOffQ + t * L::kTile + r * 128;
+#pragma unroll
+          for (int w = 0; w < D / 8; ++w) {
+            float2 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              v[i] = pair(4 * w + i);
+              v[i].x *= down;
+              v[i].y *= down;
+            }
+            // channels (0, 4), (1, 5), (2, 6), (3, 7)
+            st_shared_v4(q_row + (w >> 3) * 16384 + (((w & 7) ^ (r & 7)) << 4),
+                         pack_f16x2(v[0].x, v[2].x), pack_f16x2(v[0].y, v[2].y),
+                         pack_f16x2(v[1].x, v[3].x), pack_f16x2(v[1].y, v[3].y));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::kQFull + t));
+        }
+        const int lim = real ? kv4_sees(p, rq, row) : 0;
+        // keys that every row of this warp sees (rows past the end do not count)
+        const int all_see = __reduce_min_sync(0xffffffffu, real ? lim : 0x7fffffff);
+        float m = -3.402823466e38f, l = 0.f, v_up = 0.f;
+        for (int j = 0; j < n; ++j) {
+          const int slot = (g + j) & 3;
+          if (!(ok = wait_bounded_warp(bar(L::kSFull + t), steps & 1, limit, abort_flag, err))) break;
+          ++steps;
+          tc_fence_after();
+          // (not 0: a hidden key's score is minus infinity times it; scores in these
+          // units stay below 2^20)
+          const float f = fmaxf(factor * cs.k_up[slot], 1e-30f);
+          const float next_up = cs.v_up[slot];
+          const uint4 absent = *reinterpret_cast<const uint4*>(cs.absent[slot]);
+          const int key0 = (c.k0 + j) * 128;
+          const bool masked = key0 + 128 > all_see || (absent.x | absent.y | absent.z | absent.w) != 0;
+          uint32_t pk[64];
+          float m_new = m, l_new = 0.f;
+          bool redo = j == 0;
+          if (j == 0) {
+            // the first tile's own maximum
+            float hi = -INFINITY;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t sc[32];
+              tmem_ld_32x32b_x32(s_addr + 32 * q, sc);
+              tmem_wait_ld_regs(sc);
+              const uint32_t gone = q == 0 ? absent.x : q == 1 ? absent.y : q == 2 ? absent.z : absent.w;
+              if (masked) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (key0 + 32 * q + i >= lim || ((gone >> i) & 1u)) sc[i] = 0xff800000u;
+              }
+#pragma unroll
+              for (int i = 0; i < 32; i += 2)
+                hi = fmax3(__uint_as_float(sc[i]), __uint_as_float(sc[i + 1]), hi);
+            }
+            if (hi > -INFINITY) m_new = hi * f;
+          }
+          for (int pass = 0; pass < 2; ++pass) {
+            // exponentials against m_new, and the tile's maximum alongside
+            float hi = -INFINITY, sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t sc[32];
+              tmem_ld_32x32b_x32(s_addr + 32 * q, sc);
+              tmem_wait_ld_regs(sc);
+              if (masked) {
+                const uint32_t gone = q == 0 ? absent.x : q == 1 ? absent.y : q == 2 ? absent.z : absent.w;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (key0 + 32 * q + i >= lim || ((gone >> i) & 1u)) sc[i] = 0xff800000u;
+              }
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float a = __uint_as_float(sc[i]), b = __uint_as_float(sc[i + 1]);
+                hi = fmax3(a, b, hi);
+                const float ea = ex2_approx(fmaf(a, f, -m_new)), eb = ex2_approx(fmaf(b, f, -m_new));
+                sum0 += ea;
+                sum1 += eb;
+                pk[16 * q + i / 2] = pack_f16x2(ea, eb);
+              }
+            }
+            l_new = sum0 + sum1;
+            const bool over = hi > -INFINITY && fmaf(hi, f, -m_new) > 14.f;
+            if (pass == 1 || !__any_sync(0xffffffffu, over)) break;
+            if (over) m_new = hi * f;
+            redo = true;
+          }
+          // ---- O and l follow the reference, O also V's unit
+          float alpha = 1.f;
+          if (redo) alpha = m_new == m ? 1.f : ex2_approx(m - m_new);
+          l = fmaf(l, alpha, l_new);
+          m = m_new;
+          float o_mul = alpha;
+          if (next_up != v_up) {
+            o_mul *= v_up / next_up;
+            v_up = next_up;
+          }
+          if (j > 0 && __any_sync(0xffffffffu, o_mul != 1.f)) {
+            // (S of this tile was issued after the last P V, which is done)
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t oc[32];
+              tmem_ld_32x32b_x32(o_addr + 32 * q, oc);
+              tmem_wait_ld_regs(oc);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) oc[i] = __float_as_uint(__uint_as_float(oc[i]) * o_mul);
+              tmem_st_32x32b_x32(o_addr + 32 * q, oc);
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            tmem_st_32x32b_x32(s_addr + 32 * q, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32 * q]));
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::kPFull + t));
+        }
+        if (!ok) break;
+        g += c.most;
+        // ---- output
+        if (n > 0) {
+          if (!(ok = wait_bounded_warp(bar(L::kOFinal + t), finals & 1, limit, abort_flag, err))) break;
+          ++finals;
+          tc_fence_after();
+        }
+        const float scale_o = n == 0 || l == 0.f ? 0.f : c.whole ? v_up / l : v_up;
+        const float m_out = m == -3.402823466e38f && l == 0.f ? -INFINITY : m;
+#pragma unroll 1
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t oc[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) oc[i] = 0;
+          if (n > 0) {
+            tmem_ld_32x32b_x32(o_addr + 32 * q, oc);
+            tmem_wait_ld_regs(oc);
+          }
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {  // column 8 w + (0 .. 7) is channel 0, 4, 1, 5, 2, 6, 3, 7
+            const int ch = (i & ~7) + (i & 7) / 2 + 4 * (i & 1);
+            // (a row that sees nothing gets 0, whatever its accumulator holds)
+            v[ch] = scale_o == 0.f ? 0.f : __uint_as_float(oc[i]) * scale_o;
+          }
+          if (c.whole) {
+            if (real) {
+              uint16_t* to = static_cast<uint16_t*>(p.o) + (rq.first + tok) * p.o_st + head * p.o_sh + 32 * q;
+#pragma unroll
+              for (int i = 0; i < 32; i += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  w[k] = p.is_half ? pack_f16x2(v[i + 2 * k], v[i + 2 * k + 1])
+                                   : pack_bf16x2(v[i + 2 * k], v[i + 2 * k + 1]);
+                *reinterpret_cast<uint4*>(to + i) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
+          } else {
+            // four channels of a row together, rows beside each other
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<float4*>(part + ((8 * q + i / 4) * kChunkRows + in_tile) * 4) =
+                  make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          }
+        }
+        if (c.whole) {
+          if (real)
+            p.lse[static_cast<long long>(rq.first + tok) * p.heads + head] =
+                l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        } else {
+          part[kChunkRows * D + in_tile] = m_out;
+          part[kChunkRows * (D + 1) + in_tile] = l;
+        }
+        // the next piece's P V overwrites O only after P is written again, by
+        // these threads
+        tc_fence_before();
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, L::kTmemCols);
+}
+
+// Joins the partial results of kv4_chunk_kernel, as kv4_combine_kernel does:
+// blocks (c, y), y = 32 rows each; a lane takes a row, a warp every fourth
+// group of four channels.
+template <int D>
+__global__ void __launch_bounds__(128)
+    kv4_chunk_combine_kernel(const __grid_constant__ Kv4AttendParams p, int ctas) {
+  using L = Kv4ChunkLayout<D>;
+  __shared__ Kv4Shared sh;
+  const int cta = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  kv4_locate<kChunkRows, kChunkUnit, 4>(p, sh, cta, ctas);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (sh.found_b < 0) return;
+  const Kv4Share share(sh.total, ctas);
+  const long long cut = share.start(cta);
+  Kv4Walk<kChunkRows, kChunkUnit> walk(p, sh.found_b, sh.found_excl);
+  walk.to(p, cut);
+  const long long u0 = walk.job_start(), u1 = u0 + walk.units;
+  if (cut == u0 || share.start(cta - 1) > u0) return;
+  const int r = blockIdx.y * 32 + lane, row = walk.tile * kChunkRows + r;
+  if (row >= walk.rq.rows) return;
+  const int first = cta - 1;
+  int last = cta;
+  while (share.start(last + 1) < u1) ++last;
+  auto piece = [&](int c) {
+    return p.part + (2LL * c + (c == first && share.start(first) <= u0 ? 1 : 0)) * L::kPartFloats;
+  };
+  float top = -INFINITY, sum = 0.f;
+  for (int c = first; c <= last; ++c) top = fmaxf(top, piece(c)[kChunkRows * D + r]);
+  for (int c = first; c <= last; ++c) {
+    const float m = piece(c)[kChunkRows * D + r];
+    if (m != -INFINITY) sum = fmaf(piece(c)[kChunkRows * (D + 1) + r], ex2_approx(m - top), sum);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int tok = p.by_group(row), head = walk.h * p.group + row - tok * p.group;
+  uint16_t* to = static_cast<uint16_t*>(p.o) + (walk.rq.first + tok) * p.o_st + head * p.o_sh;
+  for (int c4 = warp; c4 < D / 4; c4 += 4) {
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = first; c <= last; ++c) {
+      const float m = piece(c)[kChunkRows * D + r];
+      if (m == -INFINITY) continue;
+      const float w = ex2_approx(m - top);
+      const float4 v = *reinterpret_cast<const float4*>(piece(c) + (c4 * kChunkRows + r) * 4);
+      o.x = fmaf(v.x, w, o.x);
+      o.y = fmaf(v.y, w, o.y);
+      o.z = fmaf(v.z, w, o.z);
+      o.w = fmaf(v.w, w, o.w);
+    }
+    const uint32_t lo = p.is_half ? pack_f16x2(o.x * inv, o.y * inv) : pack_bf16x2(o.x * inv, o.y * inv);
+    const uint32_t hi = p.is_half ? pack_f16x2(o.z * inv, o.w * inv) : pack_bf16x2(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2*>(to + 4 * c4) = make_uint2(lo, hi);
+  }
+  if (warp == 0)
+    p.lse[static_cast<long long>(walk.rq.first + tok) * p.heads + head] =
+        sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+}  // namespace fa

@@ -4,6 +4,7 @@
 
 #include "kv4.cuh"
 #include "kv4_attend.cuh"
+#include "kv4_chunk.cuh"
 #include "rotary.cuh"
 
 namespace {
@@ -98,9 +99,29 @@ fa_status store_params(fa::Kv4StoreParams* p, const void* k, const void* v, cons
   return FA_OK;
 }
 
-int attend_tiles(int max_tokens, int group) {
+// The kernel for `max_tokens` queries a request: 1 to 4 row tiles of 8 on mma
+// (kv4_attend.cuh), 0: 256 rows on tcgen05 (kv4_chunk.cuh).
+constexpr int kChunkFrom = 64;  // rows
+int attend_kind(int max_tokens, int group) {
   const long long rows = static_cast<long long>(max_tokens) * group;
-  return rows <= 24 ? static_cast<int>((rows + 7) / 8) : 4;
+  return rows >= kChunkFrom ? 0 : rows <= 24 ? static_cast<int>((rows + 7) / 8) : 4;
+}
+
+// The kernel that joins partial results, 128 threads; it may start while the
+// kernel before it still runs.
+fa_status launch_join(void (*kernel)(fa::Kv4AttendParams, int), int ctas, int rows,
+                      const fa::Kv4AttendParams& p, cudaStream_t st) {
+  LaunchTimer timer(st, FA_KERNEL_KV4_COMBINE);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas - 1), static_cast<unsigned>(rows));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute early[1];
+  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, ctas) == cudaSuccess && launched() ? FA_OK : FA_ERR_CUDA;
 }
 
 template <int D, int NT>
@@ -119,26 +140,36 @@ fa_status launch_attend(const fa::Kv4AttendParams& p, cudaStream_t st) {
     fa::kv4_attend_kernel<D, NT><<<ctas, fa::kKv4Warps * 32, L::kBytes, st>>>(p);
     if (!launched()) return FA_ERR_CUDA;
   }
-  LaunchTimer timer(st, FA_KERNEL_KV4_COMBINE);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas - 1), 2 * NT);
-  cfg.blockDim = dim3(fa::kKv4Warps * 32);
-  cfg.stream = st;
-  cudaLaunchAttribute early[1];
-  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = early;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fa::kv4_combine_kernel<D, NT>, p, ctas) == cudaSuccess && launched()
-             ? FA_OK
-             : FA_ERR_CUDA;
+  return launch_join(fa::kv4_combine_kernel<D, NT>, ctas, 2 * NT, p, st);
 }
 
-size_t attend_workspace(int d, int nt) {
+template <int D>
+fa_status launch_chunk(const fa::Kv4AttendParams& p, cudaStream_t st) {
+  using L = fa::Kv4ChunkLayout<D>;
+  static bool attr_set[kMaxDevices] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FA_ERR_CUDA;
+  if (!attr_set[dev]) {
+    if (!set_smem(fa::kv4_chunk_kernel<D>, L::kSmemAlloc)) return FA_ERR_CUDA;
+    attr_set[dev] = true;
+  }
+  const int ctas = sm_count(dev);
+  {
+    LaunchTimer timer(st, FA_KERNEL_KV4_ATTEND);
+    fa::kv4_chunk_kernel<D><<<ctas, fa::kChunkWarps * 32, L::kSmemAlloc, st>>>(p);
+    if (!launched()) return FA_ERR_CUDA;
+  }
+  return launch_join(fa::kv4_chunk_combine_kernel<D>, ctas, fa::kChunkRows / 32, p, st);
+}
+
+size_t attend_workspace(int d, int kind) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
-  const size_t per_cta = (nt == 1 ? fa::Kv4AttendLayout<128, 1>::kCtas : fa::Kv4AttendLayout<128, 2>::kCtas) * 2;
-  return static_cast<size_t>(sm_count(dev)) * per_cta * (8 * nt) * (d + 2) * sizeof(float);
+  const size_t per_cta = kind == 1 ? 2 * fa::Kv4AttendLayout<128, 1>::kCtas
+                         : kind    ? 2 * fa::Kv4AttendLayout<128, 2>::kCtas
+                                   : 2;
+  const size_t rows = kind ? 8 * kind : fa::kChunkRows;
+  return static_cast<size_t>(sm_count(dev)) * per_cta * rows * (d + 2) * sizeof(float);
 }
 
 }  // namespace
@@ -303,7 +334,7 @@ fa_status fa_kv4_gather(const void* cache, const long long* slots, void* k, void
 size_t fa_kv4_attention_workspace_size(int heads, int kv_heads, int d, int max_tokens) {
   if (heads < 1 || kv_heads < 1 || heads % kv_heads || (d != 64 && d != 128) || max_tokens < 1)
     return 0;
-  return attend_workspace(d, attend_tiles(max_tokens, heads / kv_heads));
+  return attend_workspace(d, attend_kind(max_tokens, heads / kv_heads));
 }
 
 fa_status fa_kv4_attention(const void* q, const void* cache, const int* block_table,
@@ -328,8 +359,8 @@ fa_status fa_kv4_attention(const void* q, const void* cache, const int* block_ta
     if (reinterpret_cast<uintptr_t>(x) & 3u) return FA_ERR_ALIGN;
   if (!aligned16(q) || !aligned16(cache) || !aligned16(o) || !strides_multiple(strides, 4, 8))
     return FA_ERR_ALIGN;
-  const int nt = attend_tiles(max_tokens, heads / kv_heads);
-  if (!workspace || workspace_bytes < attend_workspace(d, nt)) return FA_ERR_WORKSPACE;
+  const int kind = attend_kind(max_tokens, heads / kv_heads);
+  if (!workspace || workspace_bytes < attend_workspace(d, kind)) return FA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return FA_ERR_ALIGN;
   if (tokens == 0) return FA_OK;
   fa::Kv4AttendParams p = {};
@@ -361,15 +392,18 @@ fa_status fa_kv4_attention(const void* q, const void* cache, const int* block_ta
   p.page_tiles = fa::FastDiv::of(static_cast<uint32_t>(page_size / 16));
   p.by_group = fa::FastDiv::of(static_cast<uint32_t>(p.group));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (d == 64)
-    return nt == 1   ? launch_attend<64, 1>(p, s)
-           : nt == 2 ? launch_attend<64, 2>(p, s)
-           : nt == 3 ? launch_attend<64, 3>(p, s)
-                     : launch_attend<64, 4>(p, s);
-  return nt == 1   ? launch_attend<128, 1>(p, s)
-         : nt == 2 ? launch_attend<128, 2>(p, s)
-         : nt == 3 ? launch_attend<128, 3>(p, s)
-                   : launch_attend<128, 4>(p, s);
+  switch (d == 64 ? kind : 8 + kind) {
+    case 0: return launch_chunk<64>(p, s);
+    case 1: return launch_attend<64, 1>(p, s);
+    case 2: return launch_attend<64, 2>(p, s);
+    case 3: return launch_attend<64, 3>(p, s);
+    case 4: return launch_attend<64, 4>(p, s);
+    case 8: return launch_chunk<128>(p, s);
+    case 9: return launch_attend<128, 1>(p, s);
+    case 10: return launch_attend<128, 2>(p, s);
+    case 11: return launch_attend<128, 3>(p, s);
+    default: return launch_attend<128, 4>(p, s);
+  }
 }
 
 }  // extern "C"

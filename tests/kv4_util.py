@@ -82,7 +82,7 @@ def read_tiles(tiles, d):
     return out[0], out[2], out[1], out[3]
 
 
-def attention(q, cache, table, lengths, cu, causal, scale):
+def attention(q, cache, table, lengths, cu, causal, scale, rounded=False):
     """O, LSE in 64 bits and the largest errors the kernel's roundings allow.
 
     Where each term of the bounds comes from (u = half a step, eps / 2):
@@ -92,7 +92,11 @@ def attention(q, cache, table, lengths, cu, causal, scale):
       * P s in fp16: 2^-11 of P times at most 15 s a key, and, below fp16's
         smallest normal number, 2^-25 of the largest 15 s a key, twice that if s is
         half its reference (the sum of P is at least 1 at that scale);
-      * the output's type: u |O|.
+      * the output's type: u |O|;
+      * `rounded`: keys and values go through fp16, 2^-11 of themselves, or, below
+        its smallest normal number in units of 2^7 of the tile's largest, 2^-18 of
+        the largest: scores by 2^-11 of the sum of their terms' sizes and 2^-18 of
+        the largest key times the sum of q, the output by the same shares of V.
     """
     T, H, d = q.shape
     pages, G, blocks, _ = cache.shape
@@ -128,9 +132,14 @@ def attention(q, cache, table, lengths, cu, causal, scale):
                 oo = p @ vz
                 size = (qq.abs() @ (k.abs() + 2 * k8).T * abs(scale)).masked_fill(hidden, 0.0)
                 eta = 2.0 ** -17 * size.amax(1, keepdim=True)
+                if rounded:
+                    eta = eta + 2.0 ** -11 * size.amax(1, keepdim=True) + \
+                        2.0 ** -18 * k.abs().amax() * qq.abs().sum(1, keepdim=True) * abs(scale)
                 v8 = torch.where(hidden.all(0)[:, None], 0.0, v8)
                 to = (u * oo.abs() + 2.0 ** -11 * (p @ v8) * 15 / 8 + n * 2.0 ** -24 * v8.amax() * 15 / 8 +
                       eta * (p @ vz.abs() + oo.abs()) + 2.0 ** -20 * (p @ (vz.abs() + v8)))
+                if rounded:
+                    to = to + 2.0 ** -11 * (p @ vz.abs()) + 2.0 ** -18 * vz.abs().amax()
                 tl = eta[:, 0] + 2.0 ** -20 + 2.0 ** -22 * ll.abs()
             shape = (new, H // G)
             o[first:last, rows] = oo.reshape(*shape, d)

@@ -85,12 +85,13 @@ class Case:
         o, lse = fa.kv4_attention(self.q, self.cache, self.table, self.lens, self.cu,
                                   max_tokens=most or self.most, causal=causal, scale=scale, **kw)
         fa.check_device_error()
-        self.compare(o, lse, causal, scale)
+        group = self.q.shape[1] // self.cache.shape[1]
+        self.compare(o, lse, causal, scale, (most or self.most) * group >= 64)
         return o, lse
 
-    def compare(self, o, lse, causal, scale):
+    def compare(self, o, lse, causal, scale, rounded=False):
         wo, wl, to, tl = ref.attention(self.q, self.cache, self.table, self.lens.tolist(),
-                                       self.cu.tolist(), causal, scale)
+                                       self.cu.tolist(), causal, scale, rounded)
         T = int(self.cu[-1])
         o, lse, wo, wl, to, tl = o[:T].double(), lse[:T].double(), wo[:T], wl[:T], to[:T], tl[:T]
         empty = wl == -math.inf
@@ -114,6 +115,14 @@ SHAPES = [
     (64, 32, 1, 64, [90, 4096], [1, 2]),
     (128, 8, 2, 16, [260, 130], [260, 130]),
     (64, 2, 1, 16, [7, 3], [10, 9]),        # more queries than keys: rows that see nothing
+    # 64 rows and more: the tcgen05 kernel
+    (128, 64, 1, 16, [1], [1]),
+    (64, 1, 1, 64, [64, 0, 700], [64, 0, 65]),
+    (128, 1, 1, 16, [257], [257]),
+    (128, 4, 2, 48, [1000, 129, 2049], [33, 129, 1]),
+    (64, 6, 2, 16, [2000, 31], [100, 300]),  # rows that see nothing
+    (64, 16, 2, 128, [5000], [500]),
+    (128, 24, 8, 32, [300, 77, 1500, 2], [300, 50, 64, 2]),
 ]
 
 
@@ -201,6 +210,90 @@ def test_max_tokens_only_chooses_the_kernel():
     c = Case(64, 8, 2, 16, [300, 77], [9, 4], seed=6)
     for most in (1, 3, 5, 9, 4000):
         c.check(most=most)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_rows_one_long_request(d):
+    """Row tiles cut over many CTAs and joined."""
+    Case(d, 4, 1, 64, [9000], [70], seed=30).check()
+    Case(d, 8, 8, 64, [3000, 100], [3000, 100], seed=31).check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [0.0, -0.09, 3.0])
+@pytest.mark.parametrize("q_mult", [1.0, 2.0 ** -40, 2.0 ** 30])
+def test_many_rows_scales_and_sizes_of_q(scale, q_mult):
+    c = Case(128, 4, 2, 16, [500, 131], [60, 100], seed=9, q_mult=q_mult)
+    c.check(scale=scale / q_mult)
+
+
+@pytest.mark.gpu
+def test_many_rows_values_of_unlike_sizes():
+    """V's scales grow along the keys by up to 2^20 (O follows the unit of V), then
+    shrink; the keys' sizes change from page to page."""
+    c = Case(64, 8, 1, 16, [1100], [20], seed=12)
+    pages = (1100 + 15) // 16
+    for i in range(pages):
+        tile = c.cache[int(c.table[0, i])]
+        for at, power in ((8 * 64, (i * 7) % 4), (17 * 64, 20 * i // 40 if i < 40 else 20 - (i - 40))):
+            par = tile[..., at:at + 64].clone().view(torch.bfloat16)
+            tile[..., at:at + 64] = (par * 2.0 ** power).view(torch.uint8)
+    c.check()
+    c.check(causal=False)
+
+
+@pytest.mark.gpu
+def test_many_rows_masked_places_may_hold_anything():
+    H, d, page = 8, 128, 16
+    c = Case(d, H, 2, page, [150, 40], [50, 20], seed=14)
+    clean = c.cache.clone()
+    want = fa.kv4_attention(c.q, c.cache, c.table, c.lens, c.cu, max_tokens=50)
+    c.compare(*want, True, d ** -0.5, True)
+    bad = torch.tensor([0x7f, 0xc0, 0x80, 0x7f], dtype=torch.uint8, device="cuda")  # NaN, infinity
+    used = torch.zeros(c.pages * page, dtype=torch.bool, device="cuda")
+    for b, n in enumerate(c.lens.tolist()):
+        for t in range(n):
+            used[int(c.table[b, t // page]) * page + t % page] = True
+    for at in (8 * d, 17 * d):
+        rows = c.cache[..., at:at + d].unflatten(-1, (16, d // 64, 4))
+        rows[~used.reshape(c.pages, 1, 1, 16).expand(rows.shape[:4])] = bad
+    got = fa.kv4_attention(c.q, c.cache, c.table, c.lens, c.cu, max_tokens=50)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # token 130 of the first request (its query 30) is no number, in K and V, then in V
+    for places in ((8 * d, 17 * d), (17 * d,)):
+        c.cache.copy_(clean)
+        slot = int(c.table[0, 130 // page]) * page + 130 % page
+        for at in places:
+            c.cache[slot // page, :, slot % page // 16, at:at + d].unflatten(-1, (16, -1))[:, slot % 16] = \
+                bad.repeat(d // 64)
+        got = fa.kv4_attention(c.q, c.cache, c.table, c.lens, c.cu, max_tokens=50)
+        seen = torch.zeros(70, dtype=torch.bool, device="cuda")
+        seen[30:50] = True
+        assert torch.equal(got[0][~seen], want[0][~seen]) and torch.equal(got[1][~seen], want[1][~seen])
+        assert got[0][seen].isnan().all()
+    fa.check_device_error()
+
+
+@pytest.mark.gpu
+def test_many_rows_pages_outside_the_cache_are_reported():
+    c = Case(64, 4, 1, 16, [300], [20], seed=15)
+    keep = c.table.clone()
+    for page in (-1, c.pages, 1 << 30):
+        c.table.copy_(keep)
+        c.table[0, 3] = page
+        o, lse = fa.kv4_attention(c.q, c.cache, c.table, c.lens, c.cu, max_tokens=20, causal=False)
+        with pytest.raises(fa.FaError) as e:
+            fa.check_device_error()
+        assert e.value.status == 10
+        left = torch.cat([keep[0, :3], keep[0, 4:19]])
+        k, v, _, _ = (x[:284] for x in ref.read_tiles(c.cache[left.long(), 0].reshape(-1, 18 * 64), 64))
+        s = c.q.double() @ k.T / 8.0
+        # fp16 keys and values, output rounding: a few 2^-9 of values up to 4
+        assert (o.double() - torch.softmax(s, -1) @ v).abs().max() <= 2.0 ** -6
+        assert (lse.double() - torch.logsumexp(s, -1)).abs().max() <= 2.0 ** -8
+    c.table.copy_(keep)
+    c.check()
 
 
 @pytest.mark.gpu
