@@ -21,8 +21,8 @@
 // Warps (512 threads, one CTA an SM): 0 issues the MMAs; 4-7 put K and V
 // together (one key a thread, the next tile's codes already in registers);
 // 8-11 and 12-15 lay out the rows of Q tile 0 and 1, run their softmax (one
-// row a thread, the exponentials against the running maximum, the tile redone
-// only where a score passes it by 2^14) and write O.
+// row a thread, exponentials against a reference that moves only where a score
+// passes it by 2^14) and write O.
 //
 // Bound: the tensor cores and the softmax, as the forward kernel; the codes are
 // read once an item, an eighth of the bytes of a bf16 cache.
@@ -63,7 +63,7 @@ struct Kv4ChunkLayout {
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColS = 0, kColO = 256;  // S: 128 columns a tile, O: D
   static constexpr int kPartFloats = kChunkRows * (D + 2);
-  static constexpr uint32_t kRegsOther = 64, kRegsPut = 96, kRegsSoftmax = 176;
+  static constexpr uint32_t kRegsOther = 72, kRegsPut = 104, kRegsSoftmax = 168;
   static_assert(128 * (kRegsOther + kRegsPut + 2 * kRegsSoftmax) <= 512 * 128, "register split");
 };
 
@@ -110,6 +110,26 @@ __device__ __forceinline__ uint4 put_word(uint32_t w, uint32_t s24, uint32_t s20
   for (int i = 0; i < 4; ++i)
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r[i]) : "r"(c[i]), "r"(i & 1 ? s20 : s24), "r"(lo));
   return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// Two 32-bit operations in one instruction.
+__device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
 }
 
 // Shared memory of a CTA beside the tiles: what a key tile's factors are, by
@@ -248,50 +268,57 @@ __global__ void __launch_bounds__(kChunkWarps * 32, 1)
       const int row = threadIdx.x - 128;  // the thread's key of each tile
       const int tiles_per_page = p.page_size / 16;
       const long long page_bytes = static_cast<long long>(p.kv_heads) * tiles_per_page * T::kBytes;
-      // raw codes of one key; `there`: 0 no such key, 1 a key, 2 its page is
-      // outside the cache
+      // One key's codes and parameters, fetched in steps so that no latency shows:
+      // the page two tiles ahead, the parameters a tile ahead, the codes as soon
+      // as the last tile's are used.  `at`: the key's tile in the cache; null: no
+      // such key, or one in a page outside the cache (`gone`).
       uint32_t kc[D / 8], vc[D / 8], kp[D / 64], vp[D / 64];
-      int there = 0;
+      const uint8_t* at = nullptr;
+      bool gone = false;
+      auto page_of = [&](const ChunkPiece& c, int len, int j) {
+        const int key = (c.k0 + j) * 128 + row;
+        return j < c.most && key < len ? p.table[c.b * p.table_stride + p.page_tiles(key >> 4)] : -1;
+      };
+      auto locate = [&](const ChunkPiece& c, int len, int j, int id) {
+        const int key = (c.k0 + j) * 128 + row, tile = key >> 4;
+        const bool live = j < c.most && key < len;
+        const bool in = live && static_cast<unsigned>(id) < static_cast<unsigned>(p.pages);
+        gone = live && !in;
+        if (gone) atomicOr(&g_error_word, kErrBadPage);
+        at = in ? p.cache + id * page_bytes +
+                      (static_cast<long long>(c.h) * tiles_per_page + tile -
+                       static_cast<int>(p.page_tiles(tile)) * tiles_per_page) * T::kBytes
+                : nullptr;
+      };
       // Keys from `sure` on are hidden from some rows: 0 times a value that
       // is no finite number would reach them, so there a key that has one gets
       // values 0 and a score of NaN instead, for the rows that see it.
-      auto fetch = [&](const ChunkPiece& c, int len, int sure, int j) {
-        const int key = (c.k0 + j) * 128 + row;
-        there = key < len ? 1 : 0;
-        if (there) {
-          const int tile = key >> 4, page = p.page_tiles(tile), id = p.table[c.b * p.table_stride + page];
-          if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.pages)) {
-            there = 2;
-            atomicOr(&g_error_word, kErrBadPage);
-          } else {
-            const uint8_t* at = p.cache + id * page_bytes +
-                                (static_cast<long long>(c.h) * tiles_per_page + tile - page * tiles_per_page) * T::kBytes;
-            const uint8_t* k = at + T::kOffK + (key & 15) * T::kRow;
-            const uint8_t* v = at + T::kOffV + (key & 15) * T::kRow;
+      auto fetch_par = [&](const ChunkPiece& c, int sure, int j) {
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-              load_words<4>(k + 16 * i, *reinterpret_cast<uint32_t(*)[4]>(&kc[4 * i]));
-              load_words<4>(v + 16 * i, *reinterpret_cast<uint32_t(*)[4]>(&vc[4 * i]));
-            }
-            load_words<D / 64>(at + T::kOffKPar + (key & 15) * T::kPar, kp);
-            load_words<D / 64>(at + T::kOffVPar + (key & 15) * T::kPar, vp);
-            bool odd = false;
+        for (int i = 0; i < D / 64; ++i) kp[i] = vp[i] = 0;
+        if (!at) return;
+        load_words<D / 64>(at + T::kOffKPar + (row & 15) * T::kPar, kp);
+        load_words<D / 64>(at + T::kOffVPar + (row & 15) * T::kPar, vp);
+        if ((c.k0 + j) * 128 + row < sure) return;
+        bool odd = false;
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) odd |= !isfinite(bf16_hi(vp[i])) || !isfinite(bf16_lo(vp[i]));
-            if (odd && key >= sure) {
+        for (int i = 0; i < D / 64; ++i) odd |= !isfinite(bf16_hi(vp[i])) || !isfinite(bf16_lo(vp[i]));
+        if (odd) {
 #pragma unroll
-              for (int i = 0; i < D / 64; ++i) {
-                vp[i] = 0;
-                kp[i] = 0x7fc00000u;
-              }
-            }
+          for (int i = 0; i < D / 64; ++i) {
+            vp[i] = 0;
+            kp[i] = 0x7fc00000u;
           }
         }
-        if (there != 1) {
+      };
+      auto fetch_codes = [&](uint32_t (&code)[D / 8], int offset) {
 #pragma unroll
-          for (int i = 0; i < D / 64; ++i) kp[i] = vp[i] = 0;
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) kc[i] = vc[i] = 0;
+        for (int i = 0; i < D / 32; ++i) {
+          if (at)
+            load_words<4>(at + offset + (row & 15) * T::kRow + 16 * i,
+                          *reinterpret_cast<uint32_t(*)[4]>(&code[4 * i]));
+          else
+            code[4 * i] = code[4 * i + 1] = code[4 * i + 2] = code[4 * i + 3] = 0;
         }
       };
       // exponent of the largest value a pair of parameters stands for
@@ -305,21 +332,25 @@ __global__ void __launch_bounds__(kChunkWarps * 32, 1)
         return min(static_cast<int>(__float_as_uint(top) >> 23), 254);
       };
       const uint32_t to_row = row * 128;
-      // a key's row of a tile: chunk w of 8 channels is word w's
-      auto put = [&](uint32_t base, const uint32_t (&code)[D / 8], const uint32_t (&par)[D / 64],
-                     float unit, bool value) {
+      // the factors of a key's codes: 2^24 and 2^20 scale, lowest, in its unit
+      struct Put {
         uint32_t s24[D / 64], s20[D / 64], lo[D / 64];
+        __device__ __forceinline__ Put(const uint32_t (&par)[D / 64], float unit) {
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-          const float s = bf16_lo(par[i]) * unit, l = bf16_hi(par[i]) * unit;
-          s24[i] = pack_f16x2(s * 0x1p24f, s * 0x1p24f);
-          s20[i] = pack_f16x2(s * 0x1p20f, s * 0x1p20f);
-          lo[i] = pack_f16x2(l, l);
+          for (int i = 0; i < D / 64; ++i) {
+            const float s = bf16_lo(par[i]) * unit, l = bf16_hi(par[i]) * unit;
+            s24[i] = pack_f16x2(s * 0x1p24f, s * 0x1p24f);
+            s20[i] = pack_f16x2(s * 0x1p20f, s * 0x1p20f);
+            lo[i] = pack_f16x2(l, l);
+          }
         }
+      };
+      // a key's row of a tile: chunk w of 8 channels is word w's
+      auto put = [&](uint32_t base, const uint32_t (&code)[D / 8], const Put& f, bool value) {
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {  // place i of the row
           const int w = value ? 8 * (i % (D / 64)) + i / (D / 64) : 4 * (i % (D / 32)) + i / (D / 32);
-          const uint4 x = put_word(code[i], s24[w >> 3], s20[w >> 3], lo[w >> 3]);
+          const uint4 x = put_word(code[i], f.s24[w >> 3], f.s20[w >> 3], f.lo[w >> 3]);
           st_shared_v4(base + (w >> 3) * 16384 + to_row + (((w & 7) ^ (row & 7)) << 4), x.x, x.y,
                        x.z, x.w);
         }
@@ -332,19 +363,24 @@ __global__ void __launch_bounds__(kChunkWarps * 32, 1)
         const int units = static_cast<int>(min(static_cast<long long>(walk.units - walk.c0), u_end - u));
         const ChunkPiece c = chunk_piece(p, walk, units);
         u += units;
+        if (c.most == 0) continue;
         int v_size = 0;  // exponent of V's unit so far in this piece
-        const int sure = kv4_sees(p, walk.rq, c.row0);
-        if (c.most > 0) fetch(c, walk.rq.len, sure, 0);
+        const int len = walk.rq.len, sure = kv4_sees(p, walk.rq, c.row0);
+        locate(c, len, 0, page_of(c, len, 0));
+        fetch_par(c, sure, 0);
+        fetch_codes(kc, T::kOffK);
+        fetch_codes(vc, T::kOffV);
+        int id = page_of(c, len, 1);  // of the next tile's key
         for (int j = 0; j < c.most; ++j, ++g) {
           const int s = g % S;
           // the tile's sizes, over the four warps
           const int ek = __reduce_max_sync(0xffffffffu, size_of(kp));
           const int ev = __reduce_max_sync(0xffffffffu, size_of(vp));
-          const uint32_t gone = __ballot_sync(0xffffffffu, there == 2);
+          const uint32_t absent = __ballot_sync(0xffffffffu, gone);
           if (lane == 0) {
             cs.size[g & 1][warp - 4][0] = ek;
             cs.size[g & 1][warp - 4][1] = ev;
-            cs.absent[g & 3][warp - 4] = gone;
+            cs.absent[g & 3][warp - 4] = absent;
             mbar_arrive(bar(L::kSize));
           }
           if (!(ok = wait_bounded_warp(bar(L::kSize), g & 1, limit, abort_flag, err))) break;
@@ -358,25 +394,29 @@ __global__ void __launch_bounds__(kChunkWarps * 32, 1)
           // largest (exponents kept where both powers are normal numbers: values
           // from 2^119 on come out infinite)
           const int xk = min(max(k_size, 20), 245), xv = min(max(v_size, 20), 245);
-          const float k_unit = __uint_as_float(static_cast<uint32_t>(246 - xk) << 23);
-          const float v_unit = __uint_as_float(static_cast<uint32_t>(246 - xv) << 23);
           if (threadIdx.x == 128) {
             cs.k_up[g & 3] = __uint_as_float(static_cast<uint32_t>(xk + 8) << 23);
             cs.v_up[g & 3] = __uint_as_float(static_cast<uint32_t>(xv + 8) << 23);
           }
+          const Put k_put(kp, __uint_as_float(static_cast<uint32_t>(246 - xk) << 23));
+          const Put v_put(vp, __uint_as_float(static_cast<uint32_t>(246 - xv) << 23));
+          locate(c, len, j + 1, id);
+          fetch_par(c, sure, j + 1);
+          id = page_of(c, len, j + 2);
           if (!(ok = wait_bounded_warp(bar(L::kKEmpty + s), ((g / S) & 1) ^ 1, limit, abort_flag, err)))
             break;
-          put(sb + L::kOffK + s * L::kTile, kc, kp, k_unit, false);
+          put(sb + L::kOffK + s * L::kTile, kc, k_put, false);
+          fetch_codes(kc, T::kOffK);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(L::kKFull + s));
           if (!(ok = wait_bounded_warp(bar(L::kVEmpty + s), ((g / S) & 1) ^ 1, limit, abort_flag, err)))
             break;
-          put(sb + L::kOffV + s * L::kTile, vc, vp, v_unit, true);
+          put(sb + L::kOffV + s * L::kTile, vc, v_put, true);
+          fetch_codes(vc, T::kOffV);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(L::kVFull + s));
-          if (j + 1 < c.most) fetch(c, walk.rq.len, sure, j + 1);
         }
       }
     }
@@ -466,70 +506,73 @@ __global__ void __launch_bounds__(kChunkWarps * 32, 1)
           const uint4 absent = *reinterpret_cast<const uint4*>(cs.absent[slot]);
           const int key0 = (c.k0 + j) * 128;
           const bool masked = key0 + 128 > all_see || (absent.x | absent.y | absent.z | absent.w) != 0;
-          uint32_t pk[64];
-          float m_new = m, l_new = 0.f;
-          bool redo = j == 0;
-          if (j == 0) {
-            // the first tile's own maximum
+          // 32 columns at a time, the next ones already on their way: their
+          // maximum, and where some row's passes its reference by 2^14 the
+          // reference moves (and the probabilities of this tile already written,
+          // l, and below O follow); then exponentials, sums, fp16
+          float alpha = 1.f;  // what O is to be multiplied by
+          float2 sum = make_float2(0.f, 0.f);
+          uint32_t sc[2][32];
+          tmem_ld_32x32b_x32(s_addr, sc[0]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t(&x)[32] = sc[q & 1];
+            tmem_wait_ld_regs(x);
+            if (q < 3) tmem_ld_32x32b_x32(s_addr + 32 * (q + 1), sc[(q + 1) & 1]);
+            if (masked) {
+              const uint32_t out = q == 0 ? absent.x : q == 1 ? absent.y : q == 2 ? absent.z : absent.w;
+              const int left = lim - key0 - 32 * q;  // columns before it are seen
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i >= left || ((out >> i) & 1u)) x[i] = 0xff800000u;
+            }
             float hi = -INFINITY;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t sc[32];
-              tmem_ld_32x32b_x32(s_addr + 32 * q, sc);
-              tmem_wait_ld_regs(sc);
-              const uint32_t gone = q == 0 ? absent.x : q == 1 ? absent.y : q == 2 ? absent.z : absent.w;
-              if (masked) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (key0 + 32 * q + i >= lim || ((gone >> i) & 1u)) sc[i] = 0xff800000u;
+            for (int i = 0; i < 32; i += 2)
+              hi = fmax3(__uint_as_float(x[i]), __uint_as_float(x[i + 1]), hi);
+            const bool over = hi > -INFINITY && fmaf(hi, f, -m) > 14.f;
+            if (__any_sync(0xffffffffu, over)) {
+              float less = 1.f;
+              if (over) {
+                less = ex2_approx(m - hi * f);
+                m = hi * f;
               }
+              alpha *= less;
+              sum.x *= less;
+              sum.y *= less;
+              tmem_wait_st();
+#pragma unroll 1
+              for (int w = 0; w < q; ++w) {
+                uint32_t old[16];
+                tmem_ld_32x32b_x16(s_addr + 16 * w, old);
+                tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; i += 2)
-                hi = fmax3(__uint_as_float(sc[i]), __uint_as_float(sc[i + 1]), hi);
-            }
-            if (hi > -INFINITY) m_new = hi * f;
-          }
-          for (int pass = 0; pass < 2; ++pass) {
-            // exponentials against m_new, and the tile's maximum alongside
-            float hi = -INFINITY, sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t sc[32];
-              tmem_ld_32x32b_x32(s_addr + 32 * q, sc);
-              tmem_wait_ld_regs(sc);
-              if (masked) {
-                const uint32_t gone = q == 0 ? absent.x : q == 1 ? absent.y : q == 2 ? absent.z : absent.w;
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (key0 + 32 * q + i >= lim || ((gone >> i) & 1u)) sc[i] = 0xff800000u;
-              }
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float a = __uint_as_float(sc[i]), b = __uint_as_float(sc[i + 1]);
-                hi = fmax3(a, b, hi);
-                const float ea = ex2_approx(fmaf(a, f, -m_new)), eb = ex2_approx(fmaf(b, f, -m_new));
-                sum0 += ea;
-                sum1 += eb;
-                pk[16 * q + i / 2] = pack_f16x2(ea, eb);
+                for (int i = 0; i < 16; ++i) {
+                  asm volatile("" : "+r"(old[i]));
+                  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&old[i]));
+                  old[i] = pack_f16x2(v.x * less, v.y * less);
+                }
+                tmem_st_32x32b_x16(s_addr + 16 * w, old);
               }
             }
-            l_new = sum0 + sum1;
-            const bool over = hi > -INFINITY && fmaf(hi, f, -m_new) > 14.f;
-            if (pass == 1 || !__any_sync(0xffffffffu, over)) break;
-            if (over) m_new = hi * f;
-            redo = true;
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 y = fma_f32x2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
+                                         make_float2(f, f), make_float2(-m, -m));
+              const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+              sum = add_f32x2(sum, e);
+              pk[i / 2] = pack_f16x2(e.x, e.y);
+            }
+            tmem_st_32x32b_x16(s_addr + 16 * q, pk);
           }
-          // ---- O and l follow the reference, O also V's unit
-          float alpha = 1.f;
-          if (redo) alpha = m_new == m ? 1.f : ex2_approx(m - m_new);
-          l = fmaf(l, alpha, l_new);
-          m = m_new;
-          float o_mul = alpha;
+          l = fmaf(l, alpha, sum.x + sum.y);
+          // ---- O follows the reference and V's unit
           if (next_up != v_up) {
-            o_mul *= v_up / next_up;
+            alpha *= v_up / next_up;
             v_up = next_up;
           }
-          if (j > 0 && __any_sync(0xffffffffu, o_mul != 1.f)) {
+          if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
             // (S of this tile was issued after the last P V, which is done)
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
@@ -537,13 +580,10 @@ __global__ void __launch_bounds__(kChunkWarps * 32, 1)
               tmem_ld_32x32b_x32(o_addr + 32 * q, oc);
               tmem_wait_ld_regs(oc);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) oc[i] = __float_as_uint(__uint_as_float(oc[i]) * o_mul);
+              for (int i = 0; i < 32; ++i) oc[i] = __float_as_uint(__uint_as_float(oc[i]) * alpha);
               tmem_st_32x32b_x32(o_addr + 32 * q, oc);
             }
           }
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-            tmem_st_32x32b_x32(s_addr + 32 * q, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32 * q]));
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
