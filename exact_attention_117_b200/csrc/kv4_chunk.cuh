@@ -18,11 +18,12 @@
 // the order in which they come out of a word, (0, 4), (1, 5), (2, 6), (3, 7):
 // Q is laid out alike, and O's columns are put back in order when they leave.
 //
-// Warps (512 threads, one CTA an SM): 0 issues the MMAs; 4-7 put K and V
-// together (one key a thread, the next tile's codes already in registers);
-// 8-11 and 12-15 lay out the rows of Q tile 0 and 1, run their softmax (one
-// row a thread, exponentials against a reference that moves only where a score
-// passes it by 2^14) and write O.
+// Warps (640 threads, one CTA an SM): 0 issues the MMAs; 4-7 put K together,
+// 8-11 V (one key a thread, the next tile's codes on their way; a single group
+// of four warps for both took as long as the softmax and held it up: 477 us
+// where the case below takes TIME); 12-15 and 16-19 lay out the rows of Q tile
+// 0 and 1, run their softmax (one row a thread, exponentials against a reference
+// that moves only where a score passes it by 2^14) and write O.
 //
 // Bound: the tensor cores and the softmax, as the forward kernel; the codes are
 // read once an item, an eighth of the bytes of a bf16 cache.
@@ -34,7 +35,7 @@ namespace fa {
 
 constexpr int kChunkRows = 256;
 constexpr int kChunkUnit = 256;  // keys of a work unit
-constexpr int kChunkWarps = 16;
+constexpr int kChunkWarps = 20;
 
 template <int D>
 struct Kv4ChunkLayout {
@@ -52,8 +53,8 @@ struct Kv4ChunkLayout {
   static constexpr int kSFull = kVEmpty + kStages;  // [2]
   static constexpr int kPFull = kSFull + 2;         // [2]
   static constexpr int kOFinal = kPFull + 2;        // [2]
-  static constexpr int kSize = kOFinal + 2;         // the tile's powers of two are known
-  static constexpr int kDrain = kSize + 1;
+  static constexpr int kSize = kOFinal + 2;         // [4] the tile's sizes are known
+  static constexpr int kDrain = kSize + 4;
   static constexpr int kNumBars = kDrain + 1;
   static constexpr int kOffSlot = kOffBar + 8 * kNumBars;  // TMEM base address
   static constexpr int kOffAbort = kOffSlot + 4;
@@ -63,8 +64,9 @@ struct Kv4ChunkLayout {
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColS = 0, kColO = 256;  // S: 128 columns a tile, O: D
   static constexpr int kPartFloats = kChunkRows * (D + 2);
-  static constexpr uint32_t kRegsOther = 72, kRegsPut = 104, kRegsSoftmax = 168;
-  static_assert(128 * (kRegsOther + kRegsPut + 2 * kRegsSoftmax) <= 512 * 128, "register split");
+  // the block launches with 96 registers a thread
+  static constexpr uint32_t kRegsOther = 64, kRegsPut = 64, kRegsSoftmax = 144;
+  static_assert(128 * (kRegsOther + 2 * kRegsPut + 2 * kRegsSoftmax) <= 640 * 96, "register split");
 };
 
 // fp16 A and B, fp32 D (see idesc_bf16_f32; format 0 is fp16).
@@ -133,13 +135,165 @@ __device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
 }
 
 // Shared memory of a CTA beside the tiles: what a key tile's factors are, by
-// tile number mod 4 (the softmax is at most two tiles behind).
+// tile number mod 4.  The K warps write a tile's place once K of the tile two
+// before has been multiplied: by then the softmax and the V warps have read
+// what the place held, four tiles before.
 struct ChunkShared {
   float k_up[4];          // K in the tile is K / k_up
-  float v_up[4];          // V likewise, never smaller than before in a piece
   alignas(16) uint32_t absent[4][4];  // keys whose page lies outside the cache
-  int size[2][4][2];      // per warp: largest exponent of K and V, by tile parity
+  int size[4][4][2];      // per K warp: largest exponent of K and V
 };
+
+// The factors of a key's codes: 2^24 and 2^20 scale, lowest, in its unit.
+struct PutFactors {
+  uint32_t s24, s20, lo;
+  __device__ __forceinline__ PutFactors(uint32_t par, float unit) {
+    const float s = bf16_lo(par) * unit, l = bf16_hi(par) * unit;
+    s24 = pack_f16x2(s * 0x1p24f, s * 0x1p24f);
+    s20 = pack_f16x2(s * 0x1p20f, s * 0x1p20f);
+    lo = pack_f16x2(l, l);
+  }
+};
+
+// The four warps that put K (`value`: V) tiles together from their codes, one
+// key a thread.  One code for both: as two, it and the softmax did not stay in
+// the instruction cache (MEASURED).  A key's data comes in steps so that no latency shows: its page
+// two tiles ahead, its parameters a tile ahead, its codes as soon as the last
+// tile's are used.  The K warps read V's parameters too and say how large both
+// tiles' values are.
+template <int D>
+__device__ __forceinline__ void chunk_put(bool value, const Kv4AttendParams& p, const Kv4Shared& sh,
+                                          ChunkShared& cs, uint32_t sb, volatile int* abort_flag,
+                                          long long u_begin, long long u_end) {
+  using L = Kv4ChunkLayout<D>;
+  using T = Kv4Tile<D>;
+  constexpr int S = L::kStages;
+  constexpr unsigned int err = kErrKv4 | kErrRoleLoad;
+  auto bar = [&](int i) -> uint32_t { return sb + L::kOffBar + 8u * static_cast<uint32_t>(i); };
+  const int lane = threadIdx.x & 31, in_group = (threadIdx.x >> 5) & 3;
+  const int row = threadIdx.x & 127;  // the thread's key of each tile
+  const int tiles_per_page = p.page_size / 16;
+  uint32_t code[D / 8], kp[D / 64], vp[D / 64];
+  const uint8_t* at = nullptr;  // the key's tile in the cache, null: there is none
+  bool gone = false;            // its page lies outside the cache
+  auto page_of = [&](const ChunkPiece& c, int len, int j) {
+    const int key = (c.k0 + j) * 128 + row;
+    return j < c.most && key < len ? p.table[c.b * p.table_stride + p.page_tiles(key >> 4)] : -1;
+  };
+  auto locate = [&](const ChunkPiece& c, int len, int j, int id) {
+    const int key = (c.k0 + j) * 128 + row, tile = key >> 4;
+    const bool live = j < c.most && key < len;
+    const bool in = live && static_cast<unsigned>(id) < static_cast<unsigned>(p.pages);
+    gone = live && !in;
+    if (!value && gone) atomicOr(&g_error_word, kErrBadPage);
+    const int place = tile - static_cast<int>(p.page_tiles(tile)) * tiles_per_page;
+    at = in ? p.cache + ((static_cast<long long>(id) * p.kv_heads + c.h) * tiles_per_page + place) * T::kBytes
+            : nullptr;
+  };
+  // Keys from `sure` on are hidden from some rows: 0 times a value that is no
+  // finite number would reach them, so there a key that has one gets values 0
+  // and a score of NaN instead, for the rows that see it.
+  auto fetch_par = [&](const ChunkPiece& c, int sure, int j) {
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) kp[i] = vp[i] = 0;
+    if (!at) return;
+    if (!value) load_words<D / 64>(at + T::kOffKPar + (row & 15) * T::kPar, kp);
+    load_words<D / 64>(at + T::kOffVPar + (row & 15) * T::kPar, vp);
+    if ((c.k0 + j) * 128 + row < sure) return;
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) odd |= !isfinite(bf16_hi(vp[i])) || !isfinite(bf16_lo(vp[i]));
+    if (odd) {
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        vp[i] = 0;
+        kp[i] = 0x7fc00000u;
+      }
+    }
+  };
+  auto fetch_codes = [&]() {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      if (at)
+        load_words<4>(at + (value ? T::kOffV : T::kOffK) + (row & 15) * T::kRow + 16 * i,
+                      *reinterpret_cast<uint32_t(*)[4]>(&code[4 * i]));
+      else
+        code[4 * i] = code[4 * i + 1] = code[4 * i + 2] = code[4 * i + 3] = 0;
+    }
+  };
+  // exponent of the largest value a pair of parameters stands for
+  auto size_of = [&](const uint32_t (&par)[D / 64]) {
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      const float s = bf16_lo(par[i]), lo = bf16_hi(par[i]);
+      top = fmaxf(top, fmaxf(fabsf(lo), fabsf(fmaf(15.f, s, lo))));
+    }
+    return min(static_cast<int>(__float_as_uint(top) >> 23), 254);
+  };
+  const uint32_t base = sb + (value ? L::kOffV : L::kOffK) + row * 128, turn = (row & 7) << 4;
+  const int full = value ? L::kVFull : L::kKFull, empty = value ? L::kVEmpty : L::kKEmpty;
+
+  Kv4Walk<kChunkRows, kChunkUnit> walk(p, sh.found_b, sh.found_excl);
+  int g = 0;  // key tiles so far
+  for (long long u = u_begin; u < u_end;) {
+    walk.to(p, u);
+    const int units = static_cast<int>(min(static_cast<long long>(walk.units - walk.c0), u_end - u));
+    const ChunkPiece c = chunk_piece(p, walk, units);
+    u += units;
+    if (c.most == 0) continue;
+    int size = 0;  // exponent of the unit: K's of the tile, V's so far in this piece
+    const int len = walk.rq.len, sure = kv4_sees(p, walk.rq, c.row0);
+    locate(c, len, 0, page_of(c, len, 0));
+    fetch_par(c, sure, 0);
+    fetch_codes();
+    int id = page_of(c, len, 1);  // of the next tile's key
+    for (int j = 0; j < c.most; ++j, ++g) {
+      const int s = g % S, slot = g & 3;
+      if (!value) {
+        const int ek = __reduce_max_sync(0xffffffffu, size_of(kp));
+        const int ev = __reduce_max_sync(0xffffffffu, size_of(vp));
+        const uint32_t absent = __ballot_sync(0xffffffffu, gone);
+        if (lane == 0) {
+          cs.size[slot][in_group][0] = ek;
+          cs.size[slot][in_group][1] = ev;
+          cs.absent[slot][in_group] = absent;
+          mbar_arrive(bar(L::kSize + slot));
+        }
+      }
+      if (!wait_bounded_warp(bar(L::kSize + slot), (g >> 2) & 1, p.limit_ns, abort_flag, err)) return;
+      if (!value) size = 0;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) size = max(size, cs.size[slot][w][value ? 1 : 0]);
+      // the largest value to [2^-8, 2^-7): scale 2^24 stays below fp16's largest
+      // (exponents kept where both powers are normal numbers: values from 2^119
+      // on come out infinite)
+      const int x = min(max(size, 20), 245);
+      if (!value && row == 0) cs.k_up[slot] = __uint_as_float(static_cast<uint32_t>(x + 8) << 23);
+      const float unit = __uint_as_float(static_cast<uint32_t>(246 - x) << 23);
+      const PutFactors f0(value ? vp[0] : kp[0], unit);
+      const PutFactors f1(value ? vp[D / 64 - 1] : kp[D / 64 - 1], unit);
+      // where K's word is of the first group and V's of the second, and conversely
+      const PutFactors f01 = value ? f1 : f0, f10 = value ? f0 : f1;
+      locate(c, len, j + 1, id);
+      fetch_par(c, sure, j + 1);
+      id = page_of(c, len, j + 2);
+      if (!wait_bounded_warp(bar(empty + s), ((g / S) & 1) ^ 1, p.limit_ns, abort_flag, err)) return;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {  // place i of the row: chunk w of 8 channels is word w's
+        const int wk = 4 * (i % (D / 32)) + i / (D / 32), wv = 8 * (i % (D / 64)) + i / (D / 64);
+        const PutFactors& f = (wk >> 3) == 0 ? ((wv >> 3) == 0 ? f0 : f01) : ((wv >> 3) == 0 ? f10 : f1);
+        const uint32_t to_k = (wk >> 3) * 16384 + (wk & 7) * 16, to_v = (wv >> 3) * 16384 + (wv & 7) * 16;
+        const uint4 v = put_word(code[i], f.s24, f.s20, f.lo);
+        st_shared_v4((base + s * L::kTile + (value ? to_v : to_k)) ^ turn, v.x, v.y, v.z, v.w);
+      }
+      fetch_codes();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(full + s));
+    }
+  }
+}
 
 template <int D>
 __global__ void __launch_bounds__(kChunkWarps * 32, 1)
@@ -163,7 +317,8 @@ __global__ void __launch_bounds__(kChunkWarps * 32, 1)
     for (int i = 0; i < L::kNumBars; ++i) {
       // four warps lay out a tile, put K and V together, write P, find sizes
       const bool by_warps = i < L::kKEmpty || (i >= L::kVFull && i < L::kVEmpty) ||
-                            (i >= L::kPFull && i < L::kPFull + 2) || i == L::kSize;
+                            (i >= L::kPFull && i < L::kPFull + 2) ||
+                            (i >= L::kSize && i < L::kDrain);
       mbar_init(bar(i), by_warps ? 4 : 1);
     }
     *abort_flag = 0;
@@ -260,173 +415,16 @@ __global__ void __launch_bounds__(kChunkWarps * 32, 1)
       drain_wait(bar(L::kDrain), 0, limit);
       __syncwarp();
     }
-  } else if (warp < 8) {
+  } else if (warp < 12) {
     setmaxnreg_dec<L::kRegsPut>();
-    if (any) {
-      // ------------------------------------------- K and V from their codes
-      constexpr unsigned int err = kErrKv4 | kErrRoleLoad;
-      const int row = threadIdx.x - 128;  // the thread's key of each tile
-      const int tiles_per_page = p.page_size / 16;
-      const long long page_bytes = static_cast<long long>(p.kv_heads) * tiles_per_page * T::kBytes;
-      // One key's codes and parameters, fetched in steps so that no latency shows:
-      // the page two tiles ahead, the parameters a tile ahead, the codes as soon
-      // as the last tile's are used.  `at`: the key's tile in the cache; null: no
-      // such key, or one in a page outside the cache (`gone`).
-      uint32_t kc[D / 8], vc[D / 8], kp[D / 64], vp[D / 64];
-      const uint8_t* at = nullptr;
-      bool gone = false;
-      auto page_of = [&](const ChunkPiece& c, int len, int j) {
-        const int key = (c.k0 + j) * 128 + row;
-        return j < c.most && key < len ? p.table[c.b * p.table_stride + p.page_tiles(key >> 4)] : -1;
-      };
-      auto locate = [&](const ChunkPiece& c, int len, int j, int id) {
-        const int key = (c.k0 + j) * 128 + row, tile = key >> 4;
-        const bool live = j < c.most && key < len;
-        const bool in = live && static_cast<unsigned>(id) < static_cast<unsigned>(p.pages);
-        gone = live && !in;
-        if (gone) atomicOr(&g_error_word, kErrBadPage);
-        at = in ? p.cache + id * page_bytes +
-                      (static_cast<long long>(c.h) * tiles_per_page + tile -
-                       static_cast<int>(p.page_tiles(tile)) * tiles_per_page) * T::kBytes
-                : nullptr;
-      };
-      // Keys from `sure` on are hidden from some rows: 0 times a value that
-      // is no finite number would reach them, so there a key that has one gets
-      // values 0 and a score of NaN instead, for the rows that see it.
-      auto fetch_par = [&](const ChunkPiece& c, int sure, int j) {
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) kp[i] = vp[i] = 0;
-        if (!at) return;
-        load_words<D / 64>(at + T::kOffKPar + (row & 15) * T::kPar, kp);
-        load_words<D / 64>(at + T::kOffVPar + (row & 15) * T::kPar, vp);
-        if ((c.k0 + j) * 128 + row < sure) return;
-        bool odd = false;
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) odd |= !isfinite(bf16_hi(vp[i])) || !isfinite(bf16_lo(vp[i]));
-        if (odd) {
-#pragma unroll
-          for (int i = 0; i < D / 64; ++i) {
-            vp[i] = 0;
-            kp[i] = 0x7fc00000u;
-          }
-        }
-      };
-      auto fetch_codes = [&](uint32_t (&code)[D / 8], int offset) {
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          if (at)
-            load_words<4>(at + offset + (row & 15) * T::kRow + 16 * i,
-                          *reinterpret_cast<uint32_t(*)[4]>(&code[4 * i]));
-          else
-            code[4 * i] = code[4 * i + 1] = code[4 * i + 2] = code[4 * i + 3] = 0;
-        }
-      };
-      // exponent of the largest value a pair of parameters stands for
-      auto size_of = [&](const uint32_t (&par)[D / 64]) {
-        float top = 0.f;
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-          const float s = bf16_lo(par[i]), lo = bf16_hi(par[i]);
-          top = fmaxf(top, fmaxf(fabsf(lo), fabsf(fmaf(15.f, s, lo))));
-        }
-        return min(static_cast<int>(__float_as_uint(top) >> 23), 254);
-      };
-      const uint32_t to_row = row * 128;
-      // the factors of a key's codes: 2^24 and 2^20 scale, lowest, in its unit
-      struct Put {
-        uint32_t s24[D / 64], s20[D / 64], lo[D / 64];
-        __device__ __forceinline__ Put(const uint32_t (&par)[D / 64], float unit) {
-#pragma unroll
-          for (int i = 0; i < D / 64; ++i) {
-            const float s = bf16_lo(par[i]) * unit, l = bf16_hi(par[i]) * unit;
-            s24[i] = pack_f16x2(s * 0x1p24f, s * 0x1p24f);
-            s20[i] = pack_f16x2(s * 0x1p20f, s * 0x1p20f);
-            lo[i] = pack_f16x2(l, l);
-          }
-        }
-      };
-      // a key's row of a tile: chunk w of 8 channels is word w's
-      auto put = [&](uint32_t base, const uint32_t (&code)[D / 8], const Put& f, bool value) {
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {  // place i of the row
-          const int w = value ? 8 * (i % (D / 64)) + i / (D / 64) : 4 * (i % (D / 32)) + i / (D / 32);
-          const uint4 x = put_word(code[i], f.s24[w >> 3], f.s20[w >> 3], f.lo[w >> 3]);
-          st_shared_v4(base + (w >> 3) * 16384 + to_row + (((w & 7) ^ (row & 7)) << 4), x.x, x.y,
-                       x.z, x.w);
-        }
-      };
-      Kv4Walk<kChunkRows, kChunkUnit> walk(p, sh.found_b, sh.found_excl);
-      int g = 0;  // key tiles so far
-      bool ok = true;
-      for (long long u = u_begin; u < u_end && ok;) {
-        walk.to(p, u);
-        const int units = static_cast<int>(min(static_cast<long long>(walk.units - walk.c0), u_end - u));
-        const ChunkPiece c = chunk_piece(p, walk, units);
-        u += units;
-        if (c.most == 0) continue;
-        int v_size = 0;  // exponent of V's unit so far in this piece
-        const int len = walk.rq.len, sure = kv4_sees(p, walk.rq, c.row0);
-        locate(c, len, 0, page_of(c, len, 0));
-        fetch_par(c, sure, 0);
-        fetch_codes(kc, T::kOffK);
-        fetch_codes(vc, T::kOffV);
-        int id = page_of(c, len, 1);  // of the next tile's key
-        for (int j = 0; j < c.most; ++j, ++g) {
-          const int s = g % S;
-          // the tile's sizes, over the four warps
-          const int ek = __reduce_max_sync(0xffffffffu, size_of(kp));
-          const int ev = __reduce_max_sync(0xffffffffu, size_of(vp));
-          const uint32_t absent = __ballot_sync(0xffffffffu, gone);
-          if (lane == 0) {
-            cs.size[g & 1][warp - 4][0] = ek;
-            cs.size[g & 1][warp - 4][1] = ev;
-            cs.absent[g & 3][warp - 4] = absent;
-            mbar_arrive(bar(L::kSize));
-          }
-          if (!(ok = wait_bounded_warp(bar(L::kSize), g & 1, limit, abort_flag, err))) break;
-          int k_size = 0;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            k_size = max(k_size, cs.size[g & 1][w][0]);
-            v_size = max(v_size, cs.size[g & 1][w][1]);
-          }
-          // the largest value to [2^-8, 2^-7): scale 2^24 stays below fp16's
-          // largest (exponents kept where both powers are normal numbers: values
-          // from 2^119 on come out infinite)
-          const int xk = min(max(k_size, 20), 245), xv = min(max(v_size, 20), 245);
-          if (threadIdx.x == 128) {
-            cs.k_up[g & 3] = __uint_as_float(static_cast<uint32_t>(xk + 8) << 23);
-            cs.v_up[g & 3] = __uint_as_float(static_cast<uint32_t>(xv + 8) << 23);
-          }
-          const Put k_put(kp, __uint_as_float(static_cast<uint32_t>(246 - xk) << 23));
-          const Put v_put(vp, __uint_as_float(static_cast<uint32_t>(246 - xv) << 23));
-          locate(c, len, j + 1, id);
-          fetch_par(c, sure, j + 1);
-          id = page_of(c, len, j + 2);
-          if (!(ok = wait_bounded_warp(bar(L::kKEmpty + s), ((g / S) & 1) ^ 1, limit, abort_flag, err)))
-            break;
-          put(sb + L::kOffK + s * L::kTile, kc, k_put, false);
-          fetch_codes(kc, T::kOffK);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(L::kKFull + s));
-          if (!(ok = wait_bounded_warp(bar(L::kVEmpty + s), ((g / S) & 1) ^ 1, limit, abort_flag, err)))
-            break;
-          put(sb + L::kOffV + s * L::kTile, vc, v_put, true);
-          fetch_codes(vc, T::kOffV);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(L::kVFull + s));
-        }
-      }
-    }
+    if (any) chunk_put<D>(warp >= 8, p, sh, cs, sb, abort_flag, u_begin, u_end);
   } else {
     setmaxnreg_inc<L::kRegsSoftmax>();
     if (any) {
       // --------------------------------------------------- rows, softmax, output
       constexpr unsigned int err = kErrKv4 | kErrRoleSoftmax;
-      const int t = warp >= 12 ? 1 : 0;
-      const int r = threadIdx.x - 256 - 128 * t;  // row of the tile == TMEM lane
+      const int t = warp >= 16 ? 1 : 0;
+      const int r = threadIdx.x - 384 - 128 * t;  // row of the tile == TMEM lane
       const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t s_addr = tmem + lane_off + L::kColS + t * 128;
       const uint32_t o_addr = tmem + lane_off + L::kColO + t * D;
@@ -494,6 +492,7 @@ __global__ void __launch_bounds__(kChunkWarps * 32, 1)
         // keys that every row of this warp sees (rows past the end do not count)
         const int all_see = __reduce_min_sync(0xffffffffu, real ? lim : 0x7fffffff);
         float m = -3.402823466e38f, l = 0.f, v_up = 0.f;
+        int v_size = 0;  // V's unit, as the V warps find it
         for (int j = 0; j < n; ++j) {
           const int slot = (g + j) & 3;
           if (!(ok = wait_bounded_warp(bar(L::kSFull + t), steps & 1, limit, abort_flag, err))) break;
@@ -502,44 +501,58 @@ __global__ void __launch_bounds__(kChunkWarps * 32, 1)
           // (not 0: a hidden key's score is minus infinity times it; scores in these
           // units stay below 2^20)
           const float f = fmaxf(factor * cs.k_up[slot], 1e-30f);
-          const float next_up = cs.v_up[slot];
+#pragma unroll
+          for (int w = 0; w < 4; ++w) v_size = max(v_size, cs.size[slot][w][1]);
+          const float next_up = __uint_as_float(static_cast<uint32_t>(min(max(v_size, 20), 245) + 8) << 23);
           const uint4 absent = *reinterpret_cast<const uint4*>(cs.absent[slot]);
           const int key0 = (c.k0 + j) * 128;
           const bool masked = key0 + 128 > all_see || (absent.x | absent.y | absent.z | absent.w) != 0;
-          // 32 columns at a time, the next ones already on their way: their
-          // maximum, and where some row's passes its reference by 2^14 the
-          // reference moves (and the probabilities of this tile already written,
-          // l, and below O follow); then exponentials, sums, fp16
+          // 32 columns at a time, the next ones already on their way:
+          // exponentials against the reference, sums, fp16, and the maximum
+          // alongside; where some row's passes its reference by 2^14 the reference
+          // moves, the columns are done again, and the probabilities of this tile
+          // already written, the sums, and below O follow
           float alpha = 1.f;  // what O is to be multiplied by
           float2 sum = make_float2(0.f, 0.f);
           uint32_t sc[2][32];
           tmem_ld_32x32b_x32(s_addr, sc[0]);
-#pragma unroll
+#pragma unroll 2
           for (int q = 0; q < 4; ++q) {
             uint32_t(&x)[32] = sc[q & 1];
             tmem_wait_ld_regs(x);
             if (q < 3) tmem_ld_32x32b_x32(s_addr + 32 * (q + 1), sc[(q + 1) & 1]);
             if (masked) {
-              const uint32_t out = q == 0 ? absent.x : q == 1 ? absent.y : q == 2 ? absent.z : absent.w;
-              const int left = lim - key0 - 32 * q;  // columns before it are seen
+              const int left = min(max(lim - key0 - 32 * q, 0), 32);  // columns before it are seen
+              const uint32_t seen = (left == 32 ? ~0u : (1u << left) - 1u) & ~cs.absent[slot][q];
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (i >= left || ((out >> i) & 1u)) x[i] = 0xff800000u;
+                if (!((seen >> i) & 1u)) x[i] = 0xff800000u;
             }
-            float hi = -INFINITY;
+            uint32_t pk[16];
+            float2 before = sum;
+            for (;;) {  // (a second time only where the reference moved)
+              float hi[2] = {-INFINITY, -INFINITY};
+              sum = before;
 #pragma unroll
-            for (int i = 0; i < 32; i += 2)
-              hi = fmax3(__uint_as_float(x[i]), __uint_as_float(x[i + 1]), hi);
-            const bool over = hi > -INFINITY && fmaf(hi, f, -m) > 14.f;
-            if (__any_sync(0xffffffffu, over)) {
+              for (int i = 0; i < 32; i += 2) {
+                const float2 v = make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+                hi[(i / 2) & 1] = fmax3(v.x, v.y, hi[(i / 2) & 1]);
+                const float2 y = fma_f32x2(v, make_float2(f, f), make_float2(-m, -m));
+                const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                sum = add_f32x2(sum, e);
+                pk[i / 2] = pack_f16x2(e.x, e.y);
+              }
+              const float top = fmaxf(hi[0], hi[1]);
+              const bool over = top > -INFINITY && fmaf(top, f, -m) > 14.f;
+              if (!__any_sync(0xffffffffu, over)) break;
               float less = 1.f;
               if (over) {
-                less = ex2_approx(m - hi * f);
-                m = hi * f;
+                less = ex2_approx(m - top * f);
+                m = top * f;
               }
               alpha *= less;
-              sum.x *= less;
-              sum.y *= less;
+              before.x *= less;
+              before.y *= less;
               tmem_wait_st();
 #pragma unroll 1
               for (int w = 0; w < q; ++w) {
@@ -554,15 +567,6 @@ __global__ void __launch_bounds__(kChunkWarps * 32, 1)
                 }
                 tmem_st_32x32b_x16(s_addr + 16 * w, old);
               }
-            }
-            uint32_t pk[16];
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float2 y = fma_f32x2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
-                                         make_float2(f, f), make_float2(-m, -m));
-              const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-              sum = add_f32x2(sum, e);
-              pk[i / 2] = pack_f16x2(e.x, e.y);
             }
             tmem_st_32x32b_x16(s_addr + 16 * q, pk);
           }
