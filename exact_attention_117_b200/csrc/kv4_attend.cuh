@@ -452,8 +452,10 @@ __device__ __forceinline__ void kv4_tiles(const uint8_t* tile, const Kv4Lane<D>&
 #pragma unroll
       for (int gp = 0; gp < kGroups; ++gp)
         v = fmaf(bf16_lo(kp[i][gp]), s[i >> 1][nt][gp][c & 3], fmaf(bf16_hi(kp[i][gp]), qs[nt][gp][r], v));
-      x[nt][c] = v;
-      y[nt][c] = fmaf(v, rs[nt][r], -st.m[nt][r]);
+      // (a product and a difference, not one fused: the row's largest is then
+      // exactly 0 away from its reference, whatever its size)
+      x[nt][c] = __fmul_rn(v, rs[nt][r]);
+      y[nt][c] = __fsub_rn(x[nt][c], st.m[nt][r]);
       if (kMasked && key[i] >= lim[nt][r]) y[nt][c] = -INFINITY;
     }
 #pragma unroll
@@ -489,7 +491,7 @@ __device__ __forceinline__ void kv4_tiles(const uint8_t* tile, const Kv4Lane<D>&
         float hi = -INFINITY;
 #pragma unroll
         for (int c = r; c < 2 * kTok; c += 2)
-          if (!kMasked || key[c >> 1] < lim[nt][r]) hi = fmaxf(hi, x[nt][c] * rs[nt][r]);
+          if (!kMasked || key[c >> 1] < lim[nt][r]) hi = fmaxf(hi, x[nt][c]);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
         float f = 1.f;
@@ -509,7 +511,7 @@ __device__ __forceinline__ void kv4_tiles(const uint8_t* tile, const Kv4Lane<D>&
           }
 #pragma unroll
         for (int c = r; c < 2 * kTok; c += 2) {
-          y[nt][c] = fmaf(x[nt][c], rs[nt][r], -st.m[nt][r]);
+          y[nt][c] = __fsub_rn(x[nt][c], st.m[nt][r]);
           if (kMasked && key[c >> 1] >= lim[nt][r]) y[nt][c] = -INFINITY;
         }
       }

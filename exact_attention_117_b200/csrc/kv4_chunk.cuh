@@ -115,13 +115,13 @@ __device__ __forceinline__ uint4 put_word(uint32_t w, uint32_t s24, uint32_t s20
 }
 
 // Two 32-bit operations in one instruction.
-__device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
+__device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
   float2 r;
-  asm("{\n\t.reg .b64 x, y, z, w;\n\t"
-      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}\n"
+  asm("{\n\t.reg .b64 x, y, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}\n"
       : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
 }
 __device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kChunkWarps * 32, 1)
       constexpr unsigned int err = kErrKv4 | kErrRoleMma;
       auto issue_s = [&](int t, int g) {  // S_t = Q_t K^T, K from ring position g
         const uint32_t qa = sb + L::kOffQ + t * L::kTile, ka = sb + L::kOffK + (g % S) * L::kTile;
-#pragma unroll 2
+#pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
           mma_bf16_ss(tmem + L::kColS + t * 128, sw128_desc(qa + off, 16, 1024),
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kChunkWarps * 32, 1)
       };
       auto issue_pv = [&](int t, int g, bool first) {  // O_t (+)= P_t V
         const uint32_t va = sb + L::kOffV + (g % S) * L::kTile;
-#pragma unroll 2
+#pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           mma_bf16_ts(tmem + L::kColO + t * D, tmem + L::kColS + t * 128 + kk * 8,
                       sw128_desc(va + kk * 2048, 16384, 1024), id_o, (!first || kk > 0) ? 1u : 0u);
@@ -507,20 +507,19 @@ __global__ void __launch_bounds__(kChunkWarps * 32, 1)
           const uint4 absent = *reinterpret_cast<const uint4*>(cs.absent[slot]);
           const int key0 = (c.k0 + j) * 128;
           const bool masked = key0 + 128 > all_see || (absent.x | absent.y | absent.z | absent.w) != 0;
-          // 32 columns at a time, the next ones already on their way:
+          // 32 columns at a time (one copy of this code: unrolled with the next
+          // columns loading meanwhile it is 3 % slower, for the instruction cache):
           // exponentials against the reference, sums, fp16, and the maximum
           // alongside; where some row's passes its reference by 2^14 the reference
           // moves, the columns are done again, and the probabilities of this tile
           // already written, the sums, and below O follow
           float alpha = 1.f;  // what O is to be multiplied by
           float2 sum = make_float2(0.f, 0.f);
-          uint32_t sc[2][32];
-          tmem_ld_32x32b_x32(s_addr, sc[0]);
-#pragma unroll 2
+#pragma unroll 1
           for (int q = 0; q < 4; ++q) {
-            uint32_t(&x)[32] = sc[q & 1];
+            uint32_t x[32];
+            tmem_ld_32x32b_x32(s_addr + 32 * q, x);
             tmem_wait_ld_regs(x);
-            if (q < 3) tmem_ld_32x32b_x32(s_addr + 32 * (q + 1), sc[(q + 1) & 1]);
             if (masked) {
               const int left = min(max(lim - key0 - 32 * q, 0), 32);  // columns before it are seen
               const uint32_t seen = (left == 32 ? ~0u : (1u << left) - 1u) & ~cs.absent[slot][q];
@@ -530,25 +529,28 @@ __global__ void __launch_bounds__(kChunkWarps * 32, 1)
             }
             uint32_t pk[16];
             float2 before = sum;
-            for (;;) {  // (a second time only where the reference moved)
+            for (int pass = 0;; ++pass) {  // (a second time only where the reference moved)
               float hi[2] = {-INFINITY, -INFINITY};
               sum = before;
 #pragma unroll
               for (int i = 0; i < 32; i += 2) {
                 const float2 v = make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
                 hi[(i / 2) & 1] = fmax3(v.x, v.y, hi[(i / 2) & 1]);
-                const float2 y = fma_f32x2(v, make_float2(f, f), make_float2(-m, -m));
+                // (a product and a difference, not one fused: the row's largest is
+                // then exactly 0 away from its reference, whatever its size)
+                const float2 y = add_f32x2(mul_f32x2(v, make_float2(f, f)), make_float2(-m, -m));
                 const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
                 sum = add_f32x2(sum, e);
                 pk[i / 2] = pack_f16x2(e.x, e.y);
               }
               const float top = fmaxf(hi[0], hi[1]);
-              const bool over = top > -INFINITY && fmaf(top, f, -m) > 14.f;
-              if (!__any_sync(0xffffffffu, over)) break;
+              const bool over = top > -INFINITY && top * f - m > 14.f;
+              if (pass == 1 || !__any_sync(0xffffffffu, over)) break;
               float less = 1.f;
               if (over) {
-                less = ex2_approx(m - top * f);
-                m = top * f;
+                const float next = top * f;
+                less = ex2_approx(m - next);
+                m = next;
               }
               alpha *= less;
               before.x *= less;

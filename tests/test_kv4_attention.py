@@ -229,6 +229,22 @@ def test_many_rows_scales_and_sizes_of_q(scale, q_mult):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("new", [1, 40])
+def test_scores_beyond_all_exponents(new):
+    """Scores of 2^40 and more: one key takes each row, or, where the difference to the
+    next is lost in 32 bits, some of the largest do; nothing overflows."""
+    c = Case(128, 4, 2, 16, [300, 77], [new, new], seed=21)
+    for scale in (2.0 ** 40, -(2.0 ** 70)):
+        o, lse = fa.kv4_attention(c.q, c.cache, c.table, c.lens, c.cu, max_tokens=new, scale=scale)
+        fa.check_device_error()
+        assert o.isfinite().all() and lse.isfinite().all()
+        wl = ref.attention(c.q, c.cache, c.table, c.lens.tolist(), c.cu.tolist(), True, scale)[1]
+        # scores from fp16 keys are off by at most 2^-11 of their terms' sizes, here
+        # below 2^-3 of the largest score
+        assert ((lse.double() - wl).abs() <= 2.0 ** -3 * wl.abs().amax()).all()
+
+
+@pytest.mark.gpu
 def test_many_rows_values_of_unlike_sizes():
     """V's scales grow along the keys by up to 2^20 (O follows the unit of V), then
     shrink; the keys' sizes change from page to page."""
