@@ -335,6 +335,7 @@ struct Kv4PlanParams {
   int* status;
   long long table_stride;
   int requests, width, page_size, ring_size, max_tokens;
+  FastDiv by_page;
 };
 
 struct PlanRow {
@@ -358,24 +359,25 @@ __device__ __forceinline__ PlanRow plan_row(int old_len, int new_len, int page_s
 }
 
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanBatch = 4;  // tokens a thread looks up together
 
-// Largest i in [0, n) with cu[i] <= x (cu[0] <= x, cu not decreasing).
+// Largest i in [0, n) with cu[i] <= x (cu[0] <= x, cu not decreasing, n at most
+// 1024); without branches, so that several searches interleave.
 __device__ __forceinline__ int plan_find(const int* cu, int n, int x) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cu[mid] <= x) lo = mid;
-    else hi = mid;
-  }
-  return lo;
+  int i = 0;
+#pragma unroll
+  for (int step = kPlanThreads / 2; step > 0; step >>= 1)
+    if (i + step < n && cu[i + step] <= x) i += step;
+  return i;
 }
 
-// One cluster; every CTA scans all requests (a block-wide scan of 1024 at a
-// time, held in shared memory), and the CTAs share out the tokens and pages of
-// the chunk, each located by a binary search.  Nothing is written that another
-// CTA may still read: a popped or released page's ring and table places are
-// disjoint, and lengths and range (which may be updated in place) are written
-// after a cluster barrier.
+// One cluster; every CTA scans all requests (1024 at a time, their prefix sums
+// in shared memory), and the CTAs share out the tokens and pages, each located
+// by a binary search.  Nothing is written that another CTA may still read: a
+// popped or released page's ring and table places are disjoint, and lengths and
+// range (which may be updated in place) are written after a cluster barrier.
+//
+// Bound by latency: the loads of lengths, the scan, and the loads of pages.
 __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const __grid_constant__ Kv4PlanParams p) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
@@ -383,10 +385,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const __grid_con
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   __shared__ int s_cu[kPlanThreads + 1], s_need[kPlanThreads + 1], s_back[kPlanThreads + 1];
   __shared__ int s_old[kPlanThreads], s_held[kPlanThreads];
-  __shared__ long long w_grow[32];
-  __shared__ int w_need[32], w_back[32];
-  __shared__ long long t_grow, t_need, t_back;
-  __shared__ int s_bad;
+  __shared__ int w_sum[3][32];
+  __shared__ unsigned long long t_grow, t_need, t_back;
+  __shared__ int s_bad, s_head, s_tail;
 
   const long long limit = static_cast<long long>(p.width) * p.page_size;
   const int chunks = (p.requests + kPlanThreads - 1) / kPlanThreads;
@@ -396,126 +397,129 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const __grid_con
     t_grow = t_need = t_back = 0;
   }
   __syncthreads();
-  // totals
+  // totals; the first 1024 requests stay in registers
+  int old_len = 0, new_len = 0;
+  PlanRow row = {0, 0, 0};
   {
-    long long need = 0, back = 0, grow = 0;
+    long long grow = 0;
+    int need = 0, back = 0;
     bool bad = false;
-    for (int b = tid; b < p.requests; b += kPlanThreads) {
-      const PlanRow r = plan_row(p.old_len[b], p.new_len[b], p.page_size, limit, &bad);
-      need += r.need;
-      back += r.back;
-      grow += r.grow;
+    for (int c = chunks - 1; c >= 0; --c) {
+      const int b = c * kPlanThreads + tid;
+      row = {0, 0, 0};
+      if (b < p.requests) {
+        old_len = p.old_len[b];
+        new_len = p.new_len[b];
+        row = plan_row(old_len, new_len, p.page_size, limit, &bad);
+      }
+      need += row.need;
+      back += row.back;
+      grow += row.grow;
     }
+    need = __reduce_add_sync(0xffffffffu, need);
+    back = __reduce_add_sync(0xffffffffu, back);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      need += __shfl_xor_sync(0xffffffffu, need, o);
-      back += __shfl_xor_sync(0xffffffffu, back, o);
-      grow += __shfl_xor_sync(0xffffffffu, grow, o);
-    }
+    for (int o = 16; o; o >>= 1) grow += __shfl_xor_sync(0xffffffffu, grow, o);
     bad = __any_sync(0xffffffffu, bad);
     if (lane == 0) {
-      atomicAdd(reinterpret_cast<unsigned long long*>(&t_need), static_cast<unsigned long long>(need));
-      atomicAdd(reinterpret_cast<unsigned long long*>(&t_back), static_cast<unsigned long long>(back));
-      atomicAdd(reinterpret_cast<unsigned long long*>(&t_grow), static_cast<unsigned long long>(grow));
+      if (need) atomicAdd(&t_need, static_cast<unsigned long long>(need));
+      if (back) atomicAdd(&t_back, static_cast<unsigned long long>(back));
+      if (grow) atomicAdd(&t_grow, static_cast<unsigned long long>(grow));
       if (bad) s_bad = 1;
+    }
+    if (tid == kPlanThreads - 1) {  // (a warp with little to add)
+      s_head = head >= 0 ? static_cast<int>(head % p.ring_size) : 0;
+      s_tail = tail >= 0 ? static_cast<int>(tail % p.ring_size) : 0;
     }
   }
   __syncthreads();
-  const long long avail = tail - head;
+  const long long avail = tail - head, all_need = static_cast<long long>(t_need),
+                  all_back = static_cast<long long>(t_back), all_grow = static_cast<long long>(t_grow);
   int status = s_bad ? kPlanLength : 0;
-  if (t_need > avail) status |= kPlanPages;
-  if (t_grow > p.max_tokens) status |= kPlanTokens;
-  if (head < 0 || avail < 0 || avail > p.ring_size || avail + t_back > p.ring_size)
+  if (all_need > avail) status |= kPlanPages;
+  if (all_grow > p.max_tokens) status |= kPlanTokens;
+  if (head < 0 || avail < 0 || avail > p.ring_size || avail + all_back > p.ring_size)
     status |= kPlanRing;
   const bool ok = status == 0;
-  const int total = ok ? static_cast<int>(t_grow) : 0;
+  const int total = ok ? static_cast<int>(all_grow) : 0;
+  // place i <= ring_size behind a start
+  auto ring_at = [&](int start, int i) {
+    const int at = start + i;
+    return p.ring + (at >= p.ring_size ? at - p.ring_size : at);
+  };
 
   int base_cu = 0, base_need = 0, base_back = 0;
   for (int c = 0; c < chunks; ++c) {
     const int b0 = c * kPlanThreads, cnt = min(kPlanThreads, p.requests - b0);
-    int old_len = 0, new_len = 0;
-    PlanRow r = {0, 0, 0};
-    if (tid < cnt) {
-      old_len = p.old_len[b0 + tid];
-      new_len = p.new_len[b0 + tid];
-      bool bad = false;
-      if (ok) r = plan_row(old_len, new_len, p.page_size, limit, &bad);
+    if (c > 0) {
+      row = {0, 0, 0};
+      old_len = 0;
+      if (tid < cnt) {
+        bool bad = false;
+        old_len = p.old_len[b0 + tid];
+        row = plan_row(old_len, p.new_len[b0 + tid], p.page_size, limit, &bad);
+      }
     }
     // block-wide inclusive scan of the three counts
-    int grow = static_cast<int>(r.grow), need = r.need, back = r.back;
+    int v[3] = {ok ? static_cast<int>(row.grow) : 0, ok ? row.need : 0, ok ? row.back : 0};
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int g = __shfl_up_sync(0xffffffffu, grow, o), n = __shfl_up_sync(0xffffffffu, need, o),
-                k = __shfl_up_sync(0xffffffffu, back, o);
-      if (lane >= o) {
-        grow += g;
-        need += n;
-        back += k;
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const int x = __shfl_up_sync(0xffffffffu, v[k], o);
+        if (lane >= o) v[k] += x;
       }
-    }
     if (lane == 31) {
-      w_grow[warp] = grow;
-      w_need[warp] = need;
-      w_back[warp] = back;
-    }
-    __syncthreads();
-    if (warp == 0) {
-      int g = static_cast<int>(w_grow[lane]), n = w_need[lane], k = w_back[lane];
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int g1 = __shfl_up_sync(0xffffffffu, g, o), n1 = __shfl_up_sync(0xffffffffu, n, o),
-                  k1 = __shfl_up_sync(0xffffffffu, k, o);
-        if (lane >= o) {
-          g += g1;
-          n += n1;
-          k += k1;
-        }
-      }
-      w_grow[lane] = g;
-      w_need[lane] = n;
-      w_back[lane] = k;
+      for (int k = 0; k < 3; ++k) w_sum[k][warp] = v[k];
     }
     __syncthreads();
-    if (warp > 0) {
-      grow += static_cast<int>(w_grow[warp - 1]);
-      need += w_need[warp - 1];
-      back += w_back[warp - 1];
-    }
-    s_cu[tid + 1] = base_cu + grow;
-    s_need[tid + 1] = base_need + need;
-    s_back[tid + 1] = base_back + back;
+    const int base[3] = {base_cu, base_need, base_back};
+#pragma unroll
+    for (int k = 0; k < 3; ++k)  // the warps before this one
+      v[k] += base[k] + __reduce_add_sync(0xffffffffu, lane < warp ? w_sum[k][lane] : 0);
+    s_cu[tid + 1] = v[0];
+    s_need[tid + 1] = v[1];
+    s_back[tid + 1] = v[2];
     if (tid == 0) {
       s_cu[0] = base_cu;
       s_need[0] = base_need;
       s_back[0] = base_back;
     }
-    const int held = static_cast<int>((static_cast<long long>(old_len) + p.page_size - 1) / p.page_size);
     s_old[tid] = old_len;
-    s_held[tid] = held;
+    s_held[tid] = static_cast<int>(p.by_page(static_cast<uint32_t>(max(old_len, 0)) + p.page_size - 1));
     __syncthreads();
     const int cu_end = s_cu[cnt], need_end = s_need[cnt], back_end = s_back[cnt];
     const int step = ranks * kPlanThreads, me = rank * kPlanThreads + tid;
     if (rank == 0 && tid < cnt) p.cu_tokens[b0 + tid] = s_cu[tid];
-    for (int t = base_cu + me; t < cu_end; t += step) {
-      const int i = plan_find(s_cu, cnt, t);
-      const int pos = s_old[i] + (t - s_cu[i]);
-      const int page_i = pos / p.page_size;
-      const int page = page_i < s_held[i]
-                           ? p.table[(b0 + i) * p.table_stride + page_i]
-                           : p.ring[(head + s_need[i] + (page_i - s_held[i])) % p.ring_size];
-      p.positions[t] = pos;
-      p.slots[t] = static_cast<long long>(page) * p.page_size + (pos - page_i * p.page_size);
+    for (int t0 = base_cu + me; t0 < cu_end; t0 += kPlanBatch * step) {
+      int i[kPlanBatch], pos[kPlanBatch], in_page[kPlanBatch], page[kPlanBatch];
+#pragma unroll
+      for (int u = 0; u < kPlanBatch; ++u) i[u] = plan_find(s_cu, cnt, min(t0 + u * step, cu_end - 1));
+#pragma unroll
+      for (int u = 0; u < kPlanBatch; ++u) {
+        if (t0 + u * step >= cu_end) continue;
+        pos[u] = s_old[i[u]] + (t0 + u * step - s_cu[i[u]]);
+        const int n = static_cast<int>(p.by_page(pos[u])), held = s_held[i[u]];
+        in_page[u] = pos[u] - n * p.page_size;
+        page[u] = n < held ? p.table[(b0 + i[u]) * p.table_stride + n]
+                           : *ring_at(s_head, s_need[i[u]] + n - held);
+      }
+#pragma unroll
+      for (int u = 0; u < kPlanBatch; ++u) {
+        if (t0 + u * step >= cu_end) continue;
+        p.positions[t0 + u * step] = pos[u];
+        p.slots[t0 + u * step] = static_cast<long long>(page[u]) * p.page_size + in_page[u];
+      }
     }
     for (int k = base_need + me; k < need_end; k += step) {
       const int i = plan_find(s_need, cnt, k);
-      p.table[(b0 + i) * p.table_stride + s_held[i] + (k - s_need[i])] =
-          p.ring[(head + k) % p.ring_size];
+      p.table[(b0 + i) * p.table_stride + s_held[i] + (k - s_need[i])] = *ring_at(s_head, k);
     }
     for (int k = base_back + me; k < back_end; k += step) {
       const int i = plan_find(s_back, cnt, k);
       const int rows = s_back[i + 1] - s_back[i];
-      p.ring[(tail + k) % p.ring_size] =
-          p.table[(b0 + i) * p.table_stride + s_held[i] - rows + (k - s_back[i])];
+      *ring_at(s_tail, k) = p.table[(b0 + i) * p.table_stride + s_held[i] - rows + (k - s_back[i])];
     }
     base_cu = cu_end;
     base_need = need_end;
@@ -526,14 +530,14 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const __grid_con
     p.slots[t] = -1;
     p.positions[t] = 0;
   }
-  cluster.sync();  // every CTA has read lengths and range
+  if (ranks > 1) cluster.sync();  // every CTA has read lengths and range
   if (rank == 0) {
     for (int b = tid; b < p.requests; b += kPlanThreads)
       p.out_len[b] = ok ? p.new_len[b] : p.old_len[b];
     if (tid == 0) {
       p.cu_tokens[p.requests] = total;
-      p.out_range[0] = head + (ok ? t_need : 0);
-      p.out_range[1] = tail + (ok ? t_back : 0);
+      p.out_range[0] = head + (ok ? all_need : 0);
+      p.out_range[1] = tail + (ok ? all_back : 0);
       *p.status = status;
     }
   }

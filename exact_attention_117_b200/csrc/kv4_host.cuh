@@ -248,7 +248,8 @@ fa_status fa_kv4_plan(const int* lengths, const int* new_lengths, int* block_tab
       max_tokens < 0 || max_tokens > (1 << 30) || table_stride < width)
     return FA_ERR_SHAPE;
   if (static_cast<long long>(requests) * width > (1LL << 30) || requests > (1 << 30) ||
-      static_cast<long long>(width) * page_size > 0x7fffffffLL || ring_size > (1 << 30))
+      static_cast<long long>(width) * page_size > (1LL << 30) || page_size > (1 << 30) ||
+      ring_size > (1 << 30))
     return FA_ERR_SHAPE;
   const void* four[8] = {lengths, new_lengths, block_table, free_pages, lengths_out, cu_tokens,
                          positions, status};
@@ -275,6 +276,7 @@ fa_status fa_kv4_plan(const int* lengths, const int* new_lengths, int* block_tab
   p.page_size = page_size;
   p.ring_size = ring_size;
   p.max_tokens = max_tokens;
+  p.by_page = fa::FastDiv::of(static_cast<uint32_t>(page_size));
   // one CTA writes a few thousand tokens as fast as the launch of more takes
   const unsigned ctas = max_tokens > 2 * fa::kPlanThreads ? 8 : 1;
   cudaLaunchConfig_t cfg = {};
