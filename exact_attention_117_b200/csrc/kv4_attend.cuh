@@ -49,8 +49,10 @@ struct Kv4AttendParams {
   uint64_t limit_ns;      // of a bounded wait
 };
 
+#ifndef KV4_BT
+#define KV4_BT 4
+#endif
 constexpr int kKv4Warps = 4;
-constexpr int kKv4Chunk = 32 * kKv4Warps;  // keys of a work unit
 
 // ------------------------------------------------------------ the work's order
 // Units: (request, tile of ROWS rows, kv head, UNIT keys), keys innermost; a row
@@ -242,13 +244,15 @@ __device__ __forceinline__ void load_words(const uint8_t* at, uint32_t (&w)[W]) 
 // one load are then four adjacent rows.
 __device__ __forceinline__ int kv4_tau(int r) { return (r >> 1) + 4 * (r & 1); }
 
-template <int D, int NT>
+template <int D, int NT, int BT = KV4_BT>
 struct Kv4AttendLayout {
   static constexpr int kRows = 8 * NT;
   static constexpr int kFast = NT <= 2 ? 2 : 1;  // tiles taken together where all rows see them
   static constexpr int kCtas = NT == 1 ? 3 : 2;  // resident on an SM, by registers
-  static constexpr int kBlock = 2 * Kv4Tile<D>::kBytes;  // 32 keys: one stage
-  static constexpr int kStages = D == 64 && NT == 1 ? 5 : 4;
+  static constexpr int kTiles = BT;  // tiles of a block, one stage of a warp's ring
+  static constexpr int kUnit = 16 * kTiles * kKv4Warps;  // keys of a work unit
+  static constexpr int kBlock = kTiles * Kv4Tile<D>::kBytes;
+  static constexpr int kStages = BT == 4 ? (D == 64 ? 3 : 2) : (D == 64 && NT == 1 ? 5 : 4);
   static constexpr int kRing = kKv4Warps * kStages * kBlock;
   static constexpr int kPitch = D + 4;  // floats of a row in the merge buffer
   // the merge buffer lies over the ring, which is empty by then
@@ -598,7 +602,8 @@ __global__ void __launch_bounds__(kKv4Warps * 32, (Kv4AttendLayout<D, NT>::kCtas
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
-  constexpr int kFast = L::kFast;
+  constexpr int kFast = L::kFast, kBT = L::kTiles;
+  constexpr uint32_t kAll = (1u << kBT) - 1u;
   const Kv4Lane<D> places;
   const int ctas = gridDim.x, cta = blockIdx.x;
   const uint8_t* ring = smem + warp * kS * L::kBlock;
@@ -609,12 +614,12 @@ __global__ void __launch_bounds__(kKv4Warps * 32, (Kv4AttendLayout<D, NT>::kCtas
   if (tid == 0) abort_word = 0;
   fence_barrier_init();
   fence_proxy_async_smem();
-  kv4_locate<L::kRows, kKv4Chunk, kKv4Warps>(p, sh, cta, ctas);
+  kv4_locate<L::kRows, L::kUnit, kKv4Warps>(p, sh, cta, ctas);
   const Kv4Share share(sh.total, ctas);
   const long long u_begin = share.start(cta), u_end = share.start(cta + 1);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (u_begin >= u_end) return;
-  Kv4Walk<L::kRows, kKv4Chunk> walk(p, sh.found_b, sh.found_excl);
+  Kv4Walk<L::kRows, L::kUnit> walk(p, sh.found_b, sh.found_excl);
   const int tiles_per_page = p.page_size / 16;
   int it = 0;  // blocks this warp has taken from its ring
 
@@ -629,34 +634,33 @@ __global__ void __launch_bounds__(kKv4Warps * 32, (Kv4AttendLayout<D, NT>::kCtas
 
     // ---- fill the ring; pages of the block after next are looked up an
     // iteration ahead of their copy
-    const int tile_end = min(c1 * (kKv4Chunk / 16), (any_sees + 15) / 16);
+    const int tile_end = min(c1 * (L::kUnit / 16), (any_sees + 15) / 16);
     const int blk0 = c0 * kKv4Warps + warp;
-    const int n_blk = max(0, ((tile_end + 1) / 2 - blk0 + kKv4Warps - 1) / kKv4Warps);
+    const int n_blk = max(0, ((tile_end + kBT - 1) / kBT - blk0 + kKv4Warps - 1) / kKv4Warps);
     const int* table = p.table + b * p.table_stride;
     const uint8_t* head_base = p.cache + static_cast<long long>(h) * tiles_per_page * T::kBytes;
     const long long page_bytes = static_cast<long long>(p.kv_heads) * tiles_per_page * T::kBytes;
-    // Lane 0 looks up and copies a block's first tile, lane 1 its second; both
-    // are a block ahead with the look-up.
-    uint32_t present = 0;  // two bits a stage: its tiles are there
-    int tile = 2 * blk0 + lane, fill = it % kS;
+    // Lane i looks up and copies a block's tile i, a block ahead with the look-up.
+    uint32_t present = 0;  // a bit a tile of each stage: it is there
+    int tile = kBT * blk0 + lane, fill = it % kS;
     long long from = -1;  // the lane's next tile in the cache, -1: none
     auto look_up = [&]() {
       from = -1;
-      if (lane < 2 && tile < tile_end) {
+      if (lane < kBT && tile < tile_end) {
         const int page = p.page_tiles(tile), id = table[page];
         if (static_cast<unsigned>(id) < static_cast<unsigned>(p.pages))
           from = id * page_bytes + (tile - page * tiles_per_page) * T::kBytes;
         else
           atomicOr(&g_error_word, kErrBadPage);
       }
-      tile += 2 * kKv4Warps;
+      tile += kBT * kKv4Warps;
     };
     auto copy = [&]() {  // (a block past the end: nothing is expected)
-      const uint32_t two = __ballot_sync(0xffffffffu, from >= 0);
-      present = (present & ~(3u << (2 * fill))) | two << (2 * fill);
+      const uint32_t in = __ballot_sync(0xffffffffu, from >= 0);
+      present = (present & ~(kAll << (kBT * fill))) | in << (kBT * fill);
       const uint32_t bar = bars + 8 * fill;
-      if (lane < 2) {
-        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(two) * T::kBytes);
+      if (lane < kBT) {
+        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(in) * T::kBytes);
         if (from >= 0)
           bulk_load(ring_at + fill * L::kBlock + lane * T::kBytes, head_base + from, T::kBytes, bar);
       }
@@ -712,7 +716,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, (Kv4AttendLayout<D, NT>::kCtas
     for (int nt = 0; nt < NT; ++nt) st.m[nt][0] = st.m[nt][1] = -3.402823466e38f;  // below every score
 
     bool ok = true;
-    int i = 0, stage = it % kS, key0 = 32 * blk0;
+    int i = 0, stage = it % kS, key0 = 16 * kBT * blk0;
     uint32_t parity = (it / kS) & 1;
     for (; i < n_blk; ++i) {
       if (i + kS - 1 < n_blk) {
@@ -724,23 +728,21 @@ __global__ void __launch_bounds__(kKv4Warps * 32, (Kv4AttendLayout<D, NT>::kCtas
         break;
       }
       const uint8_t* at = ring + stage * L::kBlock;
-      const uint32_t there = (present >> (2 * stage)) & 3u;
-      if (kFast == 2 && there == 3u && key0 + 32 <= all_see) {
-        kv4_tiles<D, NT, kFast, false>(at, places, smem + L::kOffQ, qf, qs, rs, lim, key0, any_sees, st);
+      const uint32_t there = (present >> (kBT * stage)) & kAll;
+      if (there == kAll && key0 + 16 * kBT <= all_see) {
+#pragma unroll 1
+        for (int k = 0; k < kBT; k += kFast)
+          kv4_tiles<D, NT, kFast, false>(at + k * T::kBytes, places, smem + L::kOffQ, qf, qs, rs, lim,
+                                         key0 + 16 * k, any_sees, st);
       } else {
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half)
-          if ((there >> half) & 1u) {
-            if (kFast == 1 && key0 + 16 * half + 16 <= all_see)
-              kv4_tiles<D, NT, 1, false>(at + half * T::kBytes, places, smem + L::kOffQ, qf, qs, rs, lim,
-                                         key0 + 16 * half, any_sees, st);
-            else
-              kv4_tiles<D, NT, 1, true>(at + half * T::kBytes, places, smem + L::kOffQ, qf, qs, rs, lim,
-                                        key0 + 16 * half, any_sees, st);
-          }
+        for (int k = 0; k < kBT; ++k)
+          if ((there >> k) & 1u)
+            kv4_tiles<D, NT, 1, true>(at + k * T::kBytes, places, smem + L::kOffQ, qf, qs, rs, lim,
+                                      key0 + 16 * k, any_sees, st);
       }
       __syncwarp();
-      key0 += kKv4Chunk;
+      key0 += L::kUnit;
       if (++stage == kS) {
         stage = 0;
         parity ^= 1;
@@ -837,12 +839,12 @@ __global__ void __launch_bounds__(kKv4Warps * 32)
   using L = Kv4AttendLayout<D, NT>;
   __shared__ Kv4Shared sh;
   const int cta = blockIdx.x + 1, lane = threadIdx.x & 31;
-  kv4_locate<L::kRows, kKv4Chunk, kKv4Warps>(p, sh, cta, ctas);
+  kv4_locate<L::kRows, L::kUnit, kKv4Warps>(p, sh, cta, ctas);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (sh.found_b < 0) return;
   const Kv4Share share(sh.total, ctas);
   const long long cut = share.start(cta);
-  Kv4Walk<L::kRows, kKv4Chunk> walk(p, sh.found_b, sh.found_excl);
+  Kv4Walk<L::kRows, L::kUnit> walk(p, sh.found_b, sh.found_excl);
   walk.to(p, cut);
   const Kv4Req& rq = walk.rq;
   const long long u0 = walk.job_start(), u1 = u0 + walk.units;
