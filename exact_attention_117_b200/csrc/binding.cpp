@@ -112,6 +112,25 @@ Tensor empty_like_dense(const Here& here, const Tensor& t) {
                                         here.device());
 }
 
+// Vectors of int32 and int64 that share one allocation, each 16-byte aligned (an
+// allocation of its own costs a vector of a few numbers as much time as a launch).
+struct Carved {
+  Tensor base;
+  int64_t used = 0;  // bytes
+  static int64_t padded(int64_t bytes) { return (bytes + 15) / 16 * 16; }
+  Carved(const Here& here, int64_t bytes) : base(empty(here, {bytes}, at::kByte)) {}
+  Tensor take(int64_t n, at::ScalarType type) {
+    const int64_t size = type == at::kLong ? 8 : 4;
+    Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+        c10::Storage(base.storage()), base.key_set(), c10::scalarTypeToTypeMeta(type));
+    c10::TensorImpl* impl = t.unsafeGetTensorImpl();
+    impl->set_storage_offset(used / size);
+    impl->set_sizes_contiguous({n});
+    used += padded(n * size);
+    return t;
+  }
+};
+
 bool overlaps_itself(const Tensor& t, int axes) {
   for (int i = 0; i < axes; ++i)
     if (t.stride(i) == 0 && t.size(i) > 1) return true;
@@ -248,14 +267,16 @@ PyObject* plan(Args a, Py_ssize_t n) {
   vector_of(range, at::kLong, 2, "free_range must be contiguous int64 [2]");
   require(most >= 0, "max_tokens must not be negative");
   for (const Tensor* t : {&len, &want, &table, &ring, &range}) here.check(*t);
-  if (!len_out) len_out = empty(here, {R}, at::kInt);
-  if (!range_out) range_out = empty(here, {2}, at::kLong);
+  auto pad = [](int64_t bytes) { return Carved::padded(bytes); };
+  Carved from(here, pad(4 * R) + pad(16) + pad(4 * (R + 1)) + pad(8LL * most) + pad(4LL * most) + pad(4));
+  if (!len_out) len_out = from.take(R, at::kInt);
+  if (!range_out) range_out = from.take(2, at::kLong);
   vector_of(*len_out, at::kInt, R, "lengths_out must be contiguous int32 [requests]");
   vector_of(*range_out, at::kLong, 2, "free_range_out must be contiguous int64 [2]");
   here.check(*len_out);
   here.check(*range_out);
-  Tensor cu = empty(here, {R + 1}, at::kInt), slots = empty(here, {most}, at::kLong),
-         positions = empty(here, {most}, at::kInt), status = empty(here, {1}, at::kInt);
+  Tensor cu = from.take(R + 1, at::kInt), slots = from.take(most, at::kLong),
+         positions = from.take(most, at::kInt), status = from.take(1, at::kInt);
   auto ints = [](const Tensor& t) { return static_cast<int*>(t.data_ptr()); };
   auto longs = [](const Tensor& t) { return static_cast<long long*>(t.data_ptr()); };
   const int st = g_api.plan(ints(len), ints(want), ints(table),

@@ -49,9 +49,6 @@ struct Kv4AttendParams {
   uint64_t limit_ns;      // of a bounded wait
 };
 
-#ifndef KV4_BT
-#define KV4_BT 4
-#endif
 constexpr int kKv4Warps = 4;
 
 // ------------------------------------------------------------ the work's order
@@ -244,15 +241,18 @@ __device__ __forceinline__ void load_words(const uint8_t* at, uint32_t (&w)[W]) 
 // one load are then four adjacent rows.
 __device__ __forceinline__ int kv4_tau(int r) { return (r >> 1) + 4 * (r & 1); }
 
-template <int D, int NT, int BT = KV4_BT>
+template <int D, int NT>
 struct Kv4AttendLayout {
   static constexpr int kRows = 8 * NT;
   static constexpr int kFast = NT <= 2 ? 2 : 1;  // tiles taken together where all rows see them
   static constexpr int kCtas = NT == 1 ? 3 : 2;  // resident on an SM, by registers
-  static constexpr int kTiles = BT;  // tiles of a block, one stage of a warp's ring
+  // tiles of a block, one stage of a warp's ring: 4, so that the waits, look-ups
+  // and copies of a block weigh little (2: 258 -> 284 instructions a tile, 83 ->
+  // 98 us for 64 requests of 200 to 8192 keys, H=32/8 d=128)
+  static constexpr int kTiles = 4;
   static constexpr int kUnit = 16 * kTiles * kKv4Warps;  // keys of a work unit
   static constexpr int kBlock = kTiles * Kv4Tile<D>::kBytes;
-  static constexpr int kStages = BT == 4 ? (D == 64 ? 3 : 2) : (D == 64 && NT == 1 ? 5 : 4);
+  static constexpr int kStages = D == 64 ? 3 : 2;
   static constexpr int kRing = kKv4Warps * kStages * kBlock;
   static constexpr int kPitch = D + 4;  // floats of a row in the merge buffer
   // the merge buffer lies over the ring, which is empty by then
