@@ -40,6 +40,7 @@ struct Kv4AttendParams {
   const int* lengths;
   const int* cu_tokens;
   float* part;            // partial results: 2 per CTA
+  struct Kv4Cut* cuts;    // of kv4_chunk.cuh: one per CTA
   long long q_st, q_sh, o_st, o_sh;  // strides in elements
   long long table_stride;
   int requests, heads, kv_heads, group, tokens, pages, page_size, width;
@@ -245,14 +246,15 @@ template <int D, int NT>
 struct Kv4AttendLayout {
   static constexpr int kRows = 8 * NT;
   static constexpr int kFast = NT <= 2 ? 2 : 1;  // tiles taken together where all rows see them
-  static constexpr int kCtas = NT == 1 ? 3 : 2;  // resident on an SM, by registers
+  // CTAs on an SM, by registers (d = 64, drafted tokens: 3 against 2 23.6 vs 26.3 us)
+  static constexpr int kCtas = NT == 1 ? (D == 64 ? 4 : 3) : D == 64 ? 3 : 2;
   // tiles of a block, one stage of a warp's ring: 4, so that the waits, look-ups
   // and copies of a block weigh little (2: 258 -> 284 instructions a tile, 83 ->
   // 98 us for 64 requests of 200 to 8192 keys, H=32/8 d=128)
   static constexpr int kTiles = 4;
   static constexpr int kUnit = 16 * kTiles * kKv4Warps;  // keys of a work unit
   static constexpr int kBlock = kTiles * Kv4Tile<D>::kBytes;
-  static constexpr int kStages = D == 64 ? 3 : 2;
+  static constexpr int kStages = 2;
   static constexpr int kRing = kKv4Warps * kStages * kBlock;
   static constexpr int kPitch = D + 4;  // floats of a row in the merge buffer
   // the merge buffer lies over the ring, which is empty by then

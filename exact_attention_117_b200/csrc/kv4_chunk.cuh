@@ -75,6 +75,34 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n, bool b_mn_maj
          (static_cast<uint32_t>(m >> 4) << 24);
 }
 
+// What the join needs about a cut (request, row tile, head), written by the CTA
+// whose range start is the first to cut it.  (kv4_combine_kernel finds its place
+// itself, while the attention kernel still runs on other SMs; here that kernel
+// fills every SM to its end.)
+struct alignas(16) Kv4Cut {
+  int first, pieces;    // CTAs first .. first + pieces - 1 hold a piece each
+  int second;           // CTA `first` left its piece in its second place
+  int rows;             // 0: this range start joins nothing
+  int token0, row0, h;  // first query of the request, row tile's first row, head
+  int unused;
+};
+// Where CTA `cta`'s range starts inside a job of units u0 .. u1 - 1.
+__device__ __forceinline__ Kv4Cut kv4_cut(const Kv4Share& share, int cta, long long u0,
+                                          long long u1, const Kv4Req& rq, int row0, int rows, int h) {
+  Kv4Cut c = {};
+  if (share.start(cta) == u0 || share.start(cta - 1) > u0) return c;  // an earlier start cuts it
+  int last = cta;
+  while (share.start(last + 1) < u1) ++last;
+  c.first = cta - 1;
+  c.pieces = last - cta + 2;
+  c.second = share.start(cta - 1) <= u0;
+  c.rows = rows;
+  c.token0 = rq.first;
+  c.row0 = row0;
+  c.h = h;
+  return c;
+}
+
 // One cut of the work: `tiles[t]` key tiles of row tile t from key tile k0 on.
 struct ChunkPiece {
   int b, h, row0, rows, k0, tiles[2], most;
@@ -338,6 +366,17 @@ __global__ void __launch_bounds__(kChunkWarps * 32, 1)
   const long long u_begin = share.start(cta), u_end = share.start(cta + 1);
   const bool any = u_begin < u_end;
   const uint64_t limit = p.limit_ns;
+  if (threadIdx.x == 32) {  // (an idle warp's)
+    if (any) {
+      Kv4Walk<kChunkRows, kChunkUnit> walk(p, sh.found_b, sh.found_excl);
+      walk.to(p, u_begin);
+      const int row0 = walk.tile * kChunkRows;
+      p.cuts[cta] = kv4_cut(share, cta, walk.job_start(), walk.job_start() + walk.units, walk.rq, row0,
+                            min(kChunkRows, walk.rq.rows - row0), walk.h);
+    } else {
+      p.cuts[cta].rows = 0;
+    }
+  }
 
   if (warp < 4) {
     setmaxnreg_dec<L::kRegsOther>();
@@ -660,60 +699,58 @@ __global__ void __launch_bounds__(kChunkWarps * 32, 1)
   if (warp == 0) tmem_dealloc(tmem, L::kTmemCols);
 }
 
-// Joins the partial results of kv4_chunk_kernel, as kv4_combine_kernel does:
-// blocks (c, y), y = 32 rows each; a lane takes a row, a warp every fourth
-// group of four channels.
+// Joins the partial results of kv4_chunk_kernel: blocks (c, y) those of the job
+// that CTA c + 1's range start cuts, if that is the first to cut it (its Kv4Cut
+// says so), y = 32 rows each; a lane takes a row, a warp every eighth group of
+// four channels.
+constexpr int kChunkJoinWarps = 8;
 template <int D>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kChunkJoinWarps * 32)
     kv4_chunk_combine_kernel(const __grid_constant__ Kv4AttendParams p, int ctas) {
   using L = Kv4ChunkLayout<D>;
-  __shared__ Kv4Shared sh;
-  const int cta = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  kv4_locate<kChunkRows, kChunkUnit, 4>(p, sh, cta, ctas);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = blockIdx.y * 32 + lane;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (sh.found_b < 0) return;
-  const Kv4Share share(sh.total, ctas);
-  const long long cut = share.start(cta);
-  Kv4Walk<kChunkRows, kChunkUnit> walk(p, sh.found_b, sh.found_excl);
-  walk.to(p, cut);
-  const long long u0 = walk.job_start(), u1 = u0 + walk.units;
-  if (cut == u0 || share.start(cta - 1) > u0) return;
-  const int r = blockIdx.y * 32 + lane, row = walk.tile * kChunkRows + r;
-  if (row >= walk.rq.rows) return;
-  const int first = cta - 1;
-  int last = cta;
-  while (share.start(last + 1) < u1) ++last;
-  auto piece = [&](int c) {
-    return p.part + (2LL * c + (c == first && share.start(first) <= u0 ? 1 : 0)) * L::kPartFloats;
+  const Kv4Cut cut = p.cuts[blockIdx.x + 1];
+  if (r >= cut.rows) return;
+  auto piece = [&](int k) {
+    return p.part + (2LL * (cut.first + k) + (k == 0 ? cut.second : 0)) * L::kPartFloats;
   };
   float top = -INFINITY, sum = 0.f;
-  for (int c = first; c <= last; ++c) top = fmaxf(top, piece(c)[kChunkRows * D + r]);
-  for (int c = first; c <= last; ++c) {
-    const float m = piece(c)[kChunkRows * D + r];
-    if (m != -INFINITY) sum = fmaf(piece(c)[kChunkRows * (D + 1) + r], ex2_approx(m - top), sum);
+  for (int k = 0; k < cut.pieces; ++k) top = fmaxf(top, piece(k)[kChunkRows * D + r]);
+  for (int k = 0; k < cut.pieces; ++k) {
+    const float m = piece(k)[kChunkRows * D + r];
+    if (m != -INFINITY) sum = fmaf(piece(k)[kChunkRows * (D + 1) + r], ex2_approx(m - top), sum);
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int tok = p.by_group(row), head = walk.h * p.group + row - tok * p.group;
-  uint16_t* to = static_cast<uint16_t*>(p.o) + (walk.rq.first + tok) * p.o_st + head * p.o_sh;
-  for (int c4 = warp; c4 < D / 4; c4 += 4) {
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = first; c <= last; ++c) {
-      const float m = piece(c)[kChunkRows * D + r];
-      if (m == -INFINITY) continue;
-      const float w = ex2_approx(m - top);
-      const float4 v = *reinterpret_cast<const float4*>(piece(c) + (c4 * kChunkRows + r) * 4);
-      o.x = fmaf(v.x, w, o.x);
-      o.y = fmaf(v.y, w, o.y);
-      o.z = fmaf(v.z, w, o.z);
-      o.w = fmaf(v.w, w, o.w);
+  const int row = cut.row0 + r, i = p.by_group(row), head = cut.h * p.group + row - i * p.group;
+  const long long tok = cut.token0 + i;
+  uint16_t* to = static_cast<uint16_t*>(p.o) + tok * p.o_st + head * p.o_sh;
+  constexpr int kEach = D / 4 / kChunkJoinWarps;  // groups of four channels of a warp
+  float4 o[kEach] = {};
+  for (int k = 0; k < cut.pieces; ++k) {
+    const float m = piece(k)[kChunkRows * D + r];
+    if (m == -INFINITY) continue;
+    const float w = ex2_approx(m - top);
+#pragma unroll
+    for (int c = 0; c < kEach; ++c) {
+      const float4 v = *reinterpret_cast<const float4*>(
+          piece(k) + ((c * kChunkJoinWarps + warp) * kChunkRows + r) * 4);
+      o[c].x = fmaf(v.x, w, o[c].x);
+      o[c].y = fmaf(v.y, w, o[c].y);
+      o[c].z = fmaf(v.z, w, o[c].z);
+      o[c].w = fmaf(v.w, w, o[c].w);
     }
-    const uint32_t lo = p.is_half ? pack_f16x2(o.x * inv, o.y * inv) : pack_bf16x2(o.x * inv, o.y * inv);
-    const uint32_t hi = p.is_half ? pack_f16x2(o.z * inv, o.w * inv) : pack_bf16x2(o.z * inv, o.w * inv);
-    *reinterpret_cast<uint2*>(to + 4 * c4) = make_uint2(lo, hi);
+  }
+#pragma unroll
+  for (int c = 0; c < kEach; ++c) {
+    const float4 v = make_float4(o[c].x * inv, o[c].y * inv, o[c].z * inv, o[c].w * inv);
+    *reinterpret_cast<uint2*>(to + 4 * (c * kChunkJoinWarps + warp)) =
+        p.is_half ? make_uint2(pack_f16x2(v.x, v.y), pack_f16x2(v.z, v.w))
+                  : make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
   }
   if (warp == 0)
-    p.lse[static_cast<long long>(walk.rq.first + tok) * p.heads + head] =
-        sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    p.lse[tok * p.heads + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 }  // namespace fa

@@ -107,14 +107,14 @@ int attend_kind(int max_tokens, int group) {
   return rows >= kChunkFrom ? 0 : rows <= 24 ? static_cast<int>((rows + 7) / 8) : 4;
 }
 
-// The kernel that joins partial results, 128 threads; it may start while the
-// kernel before it still runs.
-fa_status launch_join(void (*kernel)(fa::Kv4AttendParams, int), int ctas, int rows,
+// The kernel that joins partial results; it may start while the kernel before it
+// still runs.
+fa_status launch_join(void (*kernel)(fa::Kv4AttendParams, int), int ctas, int rows, int threads,
                       const fa::Kv4AttendParams& p, cudaStream_t st) {
   LaunchTimer timer(st, FA_KERNEL_KV4_COMBINE);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas - 1), static_cast<unsigned>(rows));
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.stream = st;
   cudaLaunchAttribute early[1];
   early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -140,7 +140,7 @@ fa_status launch_attend(const fa::Kv4AttendParams& p, cudaStream_t st) {
     fa::kv4_attend_kernel<D, NT><<<ctas, fa::kKv4Warps * 32, L::kBytes, st>>>(p);
     if (!launched()) return FA_ERR_CUDA;
   }
-  return launch_join(fa::kv4_combine_kernel<D, NT>, ctas, 2 * NT, p, st);
+  return launch_join(fa::kv4_combine_kernel<D, NT>, ctas, 2 * NT, fa::kKv4Warps * 32, p, st);
 }
 
 template <int D>
@@ -159,17 +159,21 @@ fa_status launch_chunk(const fa::Kv4AttendParams& p, cudaStream_t st) {
     fa::kv4_chunk_kernel<D><<<ctas, fa::kChunkWarps * 32, L::kSmemAlloc, st>>>(p);
     if (!launched()) return FA_ERR_CUDA;
   }
-  return launch_join(fa::kv4_chunk_combine_kernel<D>, ctas, fa::kChunkRows / 32, p, st);
+  return launch_join(fa::kv4_chunk_combine_kernel<D>, ctas, fa::kChunkRows / 32, fa::kChunkJoinWarps * 32, p, st);
 }
 
-size_t attend_workspace(int d, int kind) {
+// Workspace: two partial results a CTA, then (kind 0) a Kv4Cut a CTA.
+struct AttendWorkspace {
+  size_t cuts_at, bytes;
+};
+AttendWorkspace attend_workspace(int d, int kind) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
-  const size_t per_cta = kind == 1 ? 2 * fa::Kv4AttendLayout<128, 1>::kCtas
-                         : kind    ? 2 * fa::Kv4AttendLayout<128, 2>::kCtas
-                                   : 2;
+  // CTAs an SM: kCtas of the layouts (up to 4, or 3 for more rows)
+  const size_t ctas = static_cast<size_t>(sm_count(dev)) * (kind == 1 ? 4 : kind ? 3 : 1);
   const size_t rows = kind ? 8 * kind : fa::kChunkRows;
-  return static_cast<size_t>(sm_count(dev)) * per_cta * rows * (d + 2) * sizeof(float);
+  const size_t part = 2 * ctas * rows * (d + 2) * sizeof(float);
+  return {part, part + (kind ? 0 : ctas * sizeof(fa::Kv4Cut))};
 }
 
 }  // namespace
@@ -336,7 +340,7 @@ fa_status fa_kv4_gather(const void* cache, const long long* slots, void* k, void
 size_t fa_kv4_attention_workspace_size(int heads, int kv_heads, int d, int max_tokens) {
   if (heads < 1 || kv_heads < 1 || heads % kv_heads || (d != 64 && d != 128) || max_tokens < 1)
     return 0;
-  return attend_workspace(d, attend_kind(max_tokens, heads / kv_heads));
+  return attend_workspace(d, attend_kind(max_tokens, heads / kv_heads)).bytes;
 }
 
 fa_status fa_kv4_attention(const void* q, const void* cache, const int* block_table,
@@ -362,7 +366,8 @@ fa_status fa_kv4_attention(const void* q, const void* cache, const int* block_ta
   if (!aligned16(q) || !aligned16(cache) || !aligned16(o) || !strides_multiple(strides, 4, 8))
     return FA_ERR_ALIGN;
   const int kind = attend_kind(max_tokens, heads / kv_heads);
-  if (!workspace || workspace_bytes < attend_workspace(d, kind)) return FA_ERR_WORKSPACE;
+  const AttendWorkspace ws = attend_workspace(d, kind);
+  if (!workspace || workspace_bytes < ws.bytes) return FA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return FA_ERR_ALIGN;
   if (tokens == 0) return FA_OK;
   fa::Kv4AttendParams p = {};
@@ -374,6 +379,7 @@ fa_status fa_kv4_attention(const void* q, const void* cache, const int* block_ta
   p.lengths = lengths;
   p.cu_tokens = cu_tokens;
   p.part = static_cast<float*>(workspace);
+  p.cuts = reinterpret_cast<fa::Kv4Cut*>(static_cast<char*>(workspace) + ws.cuts_at);
   p.q_st = strides[0];
   p.q_sh = strides[1];
   p.o_st = strides[2];
