@@ -100,11 +100,17 @@ fa_status store_params(fa::Kv4StoreParams* p, const void* k, const void* v, cons
 }
 
 // The kernel for `max_tokens` queries a request: 1 to 4 row tiles of 8 on mma
-// (kv4_attend.cuh), 0: 256 rows on tcgen05 (kv4_chunk.cuh).
-constexpr int kChunkFrom = 64;  // rows
-int attend_kind(int max_tokens, int group) {
+// (kv4_attend.cuh), 0: 256 rows on tcgen05 (kv4_chunk.cuh), whose time hardly
+// depends on the rows below 128.  us on one B200, mma / tcgen05, 16 requests of
+// 4096 keys: d = 128, 8 heads, 32 rows 60 / 91, 48 rows 96 / 91, 64 rows 98 / 92,
+// 128 rows 181 / 94; d = 64, 16 heads on 4, 64 rows 42 / 47, 96 rows 52 / 47, 128
+// rows 62 / 47; 4 requests of 32768 keys cross at the same rows.  (One request
+// of 4096 keys leaves most of the GPU idle either way, and mma is ahead up to 128
+// rows, 30 / 32 us.)
+int attend_kind(int max_tokens, int group, int d) {
   const long long rows = static_cast<long long>(max_tokens) * group;
-  return rows >= kChunkFrom ? 0 : rows <= 24 ? static_cast<int>((rows + 7) / 8) : 4;
+  if (rows >= (d == 64 ? 80 : 48)) return 0;
+  return rows <= 24 ? static_cast<int>((rows + 7) / 8) : 4;
 }
 
 // The kernel that joins partial results; it may start while the kernel before it
@@ -340,7 +346,7 @@ fa_status fa_kv4_gather(const void* cache, const long long* slots, void* k, void
 size_t fa_kv4_attention_workspace_size(int heads, int kv_heads, int d, int max_tokens) {
   if (heads < 1 || kv_heads < 1 || heads % kv_heads || (d != 64 && d != 128) || max_tokens < 1)
     return 0;
-  return attend_workspace(d, attend_kind(max_tokens, heads / kv_heads)).bytes;
+  return attend_workspace(d, attend_kind(max_tokens, heads / kv_heads, d)).bytes;
 }
 
 fa_status fa_kv4_attention(const void* q, const void* cache, const int* block_table,
@@ -365,7 +371,7 @@ fa_status fa_kv4_attention(const void* q, const void* cache, const int* block_ta
     if (reinterpret_cast<uintptr_t>(x) & 3u) return FA_ERR_ALIGN;
   if (!aligned16(q) || !aligned16(cache) || !aligned16(o) || !strides_multiple(strides, 4, 8))
     return FA_ERR_ALIGN;
-  const int kind = attend_kind(max_tokens, heads / kv_heads);
+  const int kind = attend_kind(max_tokens, heads / kv_heads, d);
   const AttendWorkspace ws = attend_workspace(d, kind);
   if (!workspace || workspace_bytes < ws.bytes) return FA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return FA_ERR_ALIGN;
