@@ -3,7 +3,7 @@
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--impl ours|reference]
                     [--workload c3|c4]
-    python bench.py --sweep all|c5|splitkv|kv_outer|bwd  (supplementary per-case lines)
+    python bench.py --sweep all|c5|splitkv|kv_outer|bwd|kv4  (supplementary per-case lines)
     python bench.py --traffic                   (cases for an ncu DRAM-bytes capture)
     python bench.py --traffic-report NCU_CSV    (that capture against the traffic model)
 
@@ -744,8 +744,9 @@ def _time_device(fn, flush, stream, warmup=3, iters=10):
 def run_sweep(args):
     """Supplementary measurements (one JSON line per case, not the headline line):
     the B*H*N = 2^20 sweep (d in {64, 128}, N in 512..8192, causal and full,
-    forward and forward+backward) and the split-KV forward on few-head,
-    long-sequence problems where one CTA per Q-tile pair leaves SMs idle."""
+    forward and forward+backward), the split-KV forward on few-head,
+    long-sequence problems where one CTA per Q-tile pair leaves SMs idle, and
+    serving steps from the paged 4-bit cache (per-kernel times)."""
     import torch
 
     from exact_attention_117_b200 import fa
@@ -895,7 +896,61 @@ def run_sweep(args):
                         x["q"], x["k"], x["v"], causal=causal, num_splits=splits, out=o, lse=lse,
                         workspace=wsp, stream=stream), flush, stream)
                     emit(f"{tag} fwd split-KV x{splits}", fwd_f / (ms * 1e-3) / 1e12, ms)
+    if args.sweep in ("all", "kv4"):
+        with category("kv4"):
+            for requests, length, new in ((1, 4096, 1), (64, 4096, 1), (4, 131072, 1), (32, 4096, 5),
+                                          (2, 16384, 1024)):
+                step = kv4_step(requests, length, new)
+                for _ in range(3):
+                    step()
+                if args.once:
+                    continue
+                ms = _time_device(step, flush, stream)
+                with fa.KernelTimer() as kt:
+                    step()
+                per = {k: round(1e3 * kt.ms[k], 1) for k in kt.ms if kt.launches[k]}
+                print(json.dumps({"sweep": f"kv4 {requests} requests of {length} keys, {new} new tokens "
+                                           "each, H=32/8 d=128", "ms": round(ms, 4), "kernel_us": per}),
+                      flush=True)
+                del step
     fa.check_device_error(stream)
+
+
+def kv4_step(requests, length, new, heads=32, kv_heads=8, d=128, page=64):
+    """One layer's serving step from the paged 4-bit cache as a callable: pages and
+    slots of the new tokens, rotary positions, append, attention.  The cache holds
+    ``length - new`` tokens of each request before (random keys and values)."""
+    import torch
+
+    from exact_attention_117_b200 import fa
+    width = -(-length // page)
+    pages = requests * width
+    cache = fa.kv4_cache(pages, kv_heads, page, d)
+    for at in range(0, pages, 256):
+        slots = torch.arange(at * page, min(at + 256, pages) * page, device="cuda")
+        k, v = (torch.randn(slots.numel(), kv_heads, d, device="cuda").bfloat16() for _ in range(2))
+        fa.kv4_append(k, v, cache, slots)
+    table = torch.randperm(pages, device="cuda").int().reshape(requests, width).contiguous()
+    held = (length - new + page - 1) // page
+    ring = table[:, held:].flatten().contiguous()
+    ring = ring if ring.numel() else torch.zeros(1, dtype=torch.int32, device="cuda")
+    free = torch.tensor([0, requests * (width - held)], device="cuda")
+    old = torch.full((requests,), length - new, dtype=torch.int32, device="cuda")
+    wanted = torch.full_like(old, length)
+    x = torch.randn(requests * new, (heads + 2 * kv_heads) * d, device="cuda").bfloat16()
+    q = x[:, :heads * d].unflatten(-1, (heads, d))
+    k, v = (x[:, (heads + i * kv_heads) * d:(heads + (i + 1) * kv_heads) * d].unflatten(-1, (kv_heads, d))
+            for i in range(2))
+    freq, amplitude = fa.rotary_frequencies(d)
+
+    def step():
+        plan = fa.kv4_plan(old, wanted, table, ring, free, page, requests * new)
+        yq, yk = fa.rotary(q.transpose(0, 1)[None], k.transpose(0, 1)[None], plan.positions, freq,
+                           amplitude=amplitude)
+        fa.kv4_append(yk[0].transpose(0, 1), v, cache, plan.slots)
+        return fa.kv4_attention(yq[0].transpose(0, 1), cache, table, plan.lengths, plan.cu_tokens,
+                                max_tokens=new)
+    return step
 
 
 TRAFFIC_N = (128, 256, 512, 1024, 2048, 4096)
@@ -993,7 +1048,7 @@ def main():
     ap.add_argument("--no-long-context", action="store_true",
                     help="skip the long-context (B=1 H=32 N=16384) leg of the default line")
     ap.add_argument("--cpu-seconds", type=float, default=12.0)
-    ap.add_argument("--sweep", choices=["all", "c5", "splitkv", "kv_outer", "bwd"], default=None,
+    ap.add_argument("--sweep", choices=["all", "c5", "splitkv", "kv_outer", "bwd", "kv4"], default=None,
                     help="supplementary per-case measurements instead of the headline line")
     ap.add_argument("--once", action="store_true",
                     help="with --sweep c5, kv_outer or bwd: run the cases once, untimed (for ncu)")

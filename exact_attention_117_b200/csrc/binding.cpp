@@ -12,6 +12,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -19,6 +20,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 #include <optional>
 #include <stdexcept>
 #include <string>
@@ -84,10 +86,20 @@ struct Here {
     require(ok && t.get_device() == index, "tensors must be on the current CUDA device");
   }
   at::Device device() const { return at::Device(at::kCUDA, index); }
-  void* stream(PyObject* o) const {  // None: the current one
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(index).stream();
+  // None: the current stream.  `made`: what this call allocated, on the current
+  // stream; on another one it must not be handed out again before the call's
+  // work there is done.
+  void* stream(PyObject* o, std::initializer_list<const Tensor*> made = {}) const {
+    const auto current = c10::cuda::getCurrentCUDAStream(index);
+    if (o == Py_None) return current.stream();
     void* p = PyLong_AsVoidPtr(o);
     if (!p && PyErr_Occurred()) throw python_error();
+    if (p != static_cast<void*>(current.stream())) {
+      const auto other = c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(p), index);
+      for (const Tensor* t : made)
+        if (t && t->numel() > 0)
+          c10::cuda::CUDACachingAllocator::recordStream(t->storage().data_ptr(), other);
+    }
     return p;
   }
 };
@@ -130,6 +142,9 @@ struct Carved {
     return t;
   }
 };
+
+// The stride of an axis; one of length 1 has none that matters.
+long long step(const Tensor& t, int axis) { return t.size(axis) > 1 ? t.stride(axis) : 0; }
 
 bool overlaps_itself(const Tensor& t, int axes) {
   for (int i = 0; i < axes; ++i)
@@ -205,8 +220,9 @@ PyObject* rotary(Args a, Py_ssize_t n) {
           "inv_freq must be a contiguous fp64 vector");
   for (const Tensor* t : {&q, &pos, &freq}) here.check(*t);
   if (k) here.check(*k);
-  if (!oq) oq = empty_like_dense(here, q);
-  if (k && !ok) ok = empty_like_dense(here, *k);
+  const bool made_q = !oq, made_k = k && !ok;
+  if (made_q) oq = empty_like_dense(here, q);
+  if (made_k) ok = empty_like_dense(here, *k);
   auto output = [&](const Tensor& o, const Tensor& x) {
     here.check(o);
     require(o.sizes() == x.sizes() && o.scalar_type() == x.scalar_type() && unit(o),
@@ -217,11 +233,11 @@ PyObject* rotary(Args a, Py_ssize_t n) {
   if (k) output(*ok, *k);
   long long strides[12] = {};
   for (int i = 0; i < 3; ++i) {
-    strides[i] = q.stride(i);
-    strides[3 + i] = oq->stride(i);
+    strides[i] = step(q, i);
+    strides[3 + i] = step(*oq, i);
     if (k) {
-      strides[6 + i] = k->stride(i);
-      strides[9 + i] = ok->stride(i);
+      strides[6 + i] = step(*k, i);
+      strides[9 + i] = step(*ok, i);
     }
   }
   const int st = g_api.rotary(
@@ -230,7 +246,7 @@ PyObject* rotary(Args a, Py_ssize_t n) {
       pos.data_ptr(), pos.scalar_type() == at::kLong, pos.dim() == 2 ? pos.stride(0) : 0,
       static_cast<const double*>(freq.data_ptr()), narrow(2 * freq.size(0)), truth(a[4]),
       static_cast<float>(number(a[5])), truth(a[9]), type_code(q.scalar_type()),
-      here.stream(a[8]));
+      here.stream(a[8], {made_q ? &*oq : nullptr, made_k ? &*ok : nullptr}));
   Tuple r(3, st);
   r.set(1, *oq);
   if (k) {
@@ -283,7 +299,8 @@ PyObject* plan(Args a, Py_ssize_t n) {
                             R < 2 ? std::max(table.stride(0), table.size(1)) : table.stride(0),
                             narrow(table.size(1)), ints(ring), narrow(ring.size(0)), longs(range),
                             narrow(R), page_size, most, ints(*len_out), longs(*range_out),
-                            ints(cu), longs(slots), ints(positions), ints(status), here.stream(a[9]));
+                            ints(cu), longs(slots), ints(positions), ints(status),
+                            here.stream(a[9], {&from.base}));
   Tuple r(7, st);
   r.set(1, *len_out);
   r.set(2, std::move(cu));
@@ -312,7 +329,7 @@ PyObject* append(Args a, Py_ssize_t n) {
   const Cache c(cache, k.size(2));
   require(c.heads == k.size(1), "keys and the cache differ in kv_heads");
   here.check(cache);
-  const long long strides[4] = {k.stride(0), k.stride(1), v.stride(0), v.stride(1)};
+  const long long strides[4] = {step(k, 0), step(k, 1), step(v, 0), step(v, 1)};
   return PyLong_FromLong(g_api.append(k.data_ptr(), v.data_ptr(), cache.data_ptr(),
                                       static_cast<const long long*>(slots.data_ptr()), k.size(0),
                                       c.heads, narrow(k.size(2)), c.pages, c.page_size, strides,
@@ -333,15 +350,17 @@ PyObject* gather(Args a, Py_ssize_t n) {
   here.check(cache);
   here.check(slots);
   const int64_t T = slots.size(0);
-  if (!k) k = empty(here, {T, c.heads, d}, at::kBFloat16);
-  if (!v) v = empty(here, {T, c.heads, d}, at::kBFloat16);
+  const bool made_k = !k, made_v = !v;
+  if (made_k) k = empty(here, {T, c.heads, d}, at::kBFloat16);
+  if (made_v) v = empty(here, {T, c.heads, d}, at::kBFloat16);
   check_rows(here, *k, *v, slots);
   require(k->size(1) == c.heads && k->size(2) == d, "outputs must be bf16 [tokens, kv_heads, d]");
   require(!overlaps_itself(*k, 2) && !overlaps_itself(*v, 2), "outputs must not overlap themselves");
-  const long long strides[4] = {k->stride(0), k->stride(1), v->stride(0), v->stride(1)};
+  const long long strides[4] = {step(*k, 0), step(*k, 1), step(*v, 0), step(*v, 1)};
   const int st = g_api.gather(cache.data_ptr(), static_cast<const long long*>(slots.data_ptr()),
                               k->data_ptr(), v->data_ptr(), T, c.heads, narrow(d), c.pages,
-                              c.page_size, strides, here.stream(a[4]));
+                              c.page_size, strides,
+                              here.stream(a[4], {made_k ? &*k : nullptr, made_v ? &*v : nullptr}));
   Tuple r(3, st);
   r.set(1, *k);
   r.set(2, *v);
@@ -373,21 +392,22 @@ PyObject* attention(Args a, Py_ssize_t n) {
   for (const Tensor* t : {&q, &cache, &table, &len, &cu}) here.check(*t);
   const int most = narrow(integer(a[5]));
   const double scale = a[7] == Py_None ? 1.0 / std::sqrt(static_cast<double>(d)) : number(a[7]);
-  if (!out) out = empty_like_dense(here, q);
-  if (!lse) lse = empty(here, {T, heads}, at::kFloat);
+  const bool made_out = !out, made_lse = !lse, made_ws = !ws;
+  if (made_out) out = empty_like_dense(here, q);
+  if (made_lse) lse = empty(here, {T, heads}, at::kFloat);
   require(out->sizes() == q.sizes() && out->scalar_type() == q.scalar_type() && unit(*out) &&
               !overlaps_itself(*out, 2),
           "the output must have q's shape, dtype, a contiguous d and rows of its own");
   require(lse->scalar_type() == at::kFloat && lse->dim() == 2 && lse->size(0) == T &&
               lse->size(1) == heads && lse->is_contiguous(),
           "lse must be a contiguous fp32 [tokens, heads] tensor");
-  if (!ws) {
+  if (made_ws) {
     const size_t need = g_api.workspace_size(narrow(heads), c.heads, narrow(d), most);
     ws = empty(here, {static_cast<int64_t>(std::max<size_t>(need, 16))}, at::kByte);
   }
   require(ws->is_contiguous(), "the workspace must be contiguous");
   for (const Tensor* t : {&*out, &*lse, &*ws}) here.check(*t);
-  const long long strides[4] = {q.stride(0), q.stride(1), out->stride(0), out->stride(1)};
+  const long long strides[4] = {step(q, 0), step(q, 1), step(*out, 0), step(*out, 1)};
   const int st = g_api.attention(
       q.data_ptr(), cache.data_ptr(), static_cast<const int*>(table.data_ptr()),
       static_cast<const int*>(len.data_ptr()), static_cast<const int*>(cu.data_ptr()),
@@ -395,7 +415,8 @@ PyObject* attention(Args a, Py_ssize_t n) {
       c.heads, narrow(d), c.pages, c.page_size, narrow(table.size(1)),
       R < 2 ? std::max(table.stride(0), table.size(1)) : table.stride(0), strides, most, truth(a[6]),
       static_cast<float>(scale), type_code(q.scalar_type()), ws->data_ptr(), ws->nbytes(),
-      here.stream(a[11]));
+      here.stream(a[11], {made_out ? &*out : nullptr, made_lse ? &*lse : nullptr,
+                          made_ws ? &*ws : nullptr}));
   Tuple r(3, st);
   r.set(1, *out);
   r.set(2, *lse);

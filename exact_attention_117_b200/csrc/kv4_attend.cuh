@@ -217,12 +217,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // conversion (adding 1024 under the bits and taking it off again costs another
 // instruction a pair).  The factor 16 is taken out of q beforehand and of O
 // afterwards, 2^24 out of the scores' factor and of O.
-__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&h)[4]) {
+// flip: all ones for 15 - n in place of n (no further instruction), else 0.
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&h)[4], uint32_t flip = 0) {
   const uint32_t w8 = w >> 8;
-  h[0] = w & 0x000f000fu;
-  h[1] = w & 0x00f000f0u;
-  h[2] = w8 & 0x000f000fu;
-  h[3] = w8 & 0x00f000f0u;
+  h[0] = (w ^ flip) & 0x000f000fu;
+  h[1] = (w ^ flip) & 0x00f000f0u;
+  h[2] = (w8 ^ flip) & 0x000f000fu;
+  h[3] = (w8 ^ flip) & 0x00f000f0u;
 }
 
 template <int W>
@@ -392,6 +393,13 @@ struct Kv4Lane {
 
 // kTiles tiles of 16 adjacent keys from shared memory.  kMasked: some row does
 // not see all of them (keys no row sees may hold anything).
+//
+// Every second tile takes V as highest - s (15 - n) in place of lowest + s n: the
+// sums of P s n that the matrix instructions add up, all of one sign, then cancel
+// from tile to tile.  Over a long context O is a small difference of those sums
+// and of P lowest, and their own roundings would show in it (2 million keys of
+// one head: O off by 2.4e-3 of itself without this, 1.7e-3 with it, 1.66e-3 of
+// which is its rounding to bf16; 131072 keys 1.70e-3 either way).
 template <int D, int NT, int kTiles, bool kMasked>
 __device__ __forceinline__ void kv4_tiles(const uint8_t* tile, const Kv4Lane<D>& at,
                                           const uint8_t* q_smem,
@@ -435,6 +443,7 @@ __device__ __forceinline__ void kv4_tiles(const uint8_t* tile, const Kv4Lane<D>&
       }
     }
   }
+  auto odd = [&](int u) { return kTiles == 2 ? u == 1 : ((key0 >> 4) & 1) != 0; };
   int key[kTok];
   float vs[kTok][kGroups], vl[kTok][kGroups], x[NT][2 * kTok], y[NT][2 * kTok];
   float most = 0.f;
@@ -444,8 +453,9 @@ __device__ __forceinline__ void kv4_tiles(const uint8_t* tile, const Kv4Lane<D>&
     const bool gone = kMasked && key[i] >= any_sees;
 #pragma unroll
     for (int gp = 0; gp < kGroups; ++gp) {
-      vs[i][gp] = gone ? 0.f : bf16_lo(vp[i][gp]) * st.vinv;
-      vl[i][gp] = gone ? 0.f : bf16_hi(vp[i][gp]);
+      const float s_v = bf16_lo(vp[i][gp]), lowest = bf16_hi(vp[i][gp]);
+      vs[i][gp] = gone ? 0.f : s_v * st.vinv;
+      vl[i][gp] = gone ? 0.f : odd(i >> 1) ? fmaf(15.f, s_v, lowest) : lowest;
     }
     most = kGroups == 2 ? fmax3(vs[i][0], vs[i][kGroups - 1], most) : fmaxf(vs[i][0], most);
   }
@@ -540,7 +550,7 @@ __device__ __forceinline__ void kv4_tiles(const uint8_t* tile, const Kv4Lane<D>&
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const bool hidden = kMasked && key[i] >= lim[nt][r];
-          pv[r] = hidden ? 0.f : e[2 * i + r] * vs[i][gp];
+          pv[r] = hidden ? 0.f : e[2 * i + r] * (odd(i >> 1) ? -vs[i][gp] : vs[i][gp]);
           st.lo_sum[nt][gp][r] = hidden ? st.lo_sum[nt][gp][r]
                                         : fmaf(e[2 * i + r], vl[i][gp], st.lo_sum[nt][gp][r]);
         }
@@ -560,8 +570,9 @@ __device__ __forceinline__ void kv4_tiles(const uint8_t* tile, const Kv4Lane<D>&
       for (int half = 0; half < 2; ++half) {
         const uint32_t sel = half ? 0x7632u : 0x5410u;
         uint32_t a[4], c[4];
-        codes_f16(__byte_perm(vw[0][j], vw[1][j], sel), a);
-        codes_f16(__byte_perm(vw[2][j], vw[3][j], sel), c);
+        const uint32_t flip = odd(u) ? ~0u : 0u;
+        codes_f16(__byte_perm(vw[0][j], vw[1][j], sel), a, flip);
+        codes_f16(__byte_perm(vw[2][j], vw[3][j], sel), c, flip);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const uint32_t b0 = pb[u][nt][j][0], b1 = pb[u][nt][j][1];

@@ -19,14 +19,22 @@
 // Q is laid out alike, and O's columns are put back in order when they leave.
 //
 // Warps (640 threads, one CTA an SM): 0 issues the MMAs; 4-7 put K together,
-// 8-11 V (one key a thread, the next tile's codes on their way; a single group
-// of four warps for both took as long as the softmax and held it up: 477 us
-// where the case below takes TIME); 12-15 and 16-19 lay out the rows of Q tile
-// 0 and 1, run their softmax (one row a thread, exponentials against a reference
-// that moves only where a score passes it by 2^14) and write O.
+// 8-11 V (one key a thread, the next tile's codes on their way); 12-15 and 16-19
+// lay out the rows of Q tile 0 and 1, run their softmax (one row a thread,
+// exponentials against a reference that moves only where a score passes it by
+// 2^14) and write O.
 //
-// Bound: the tensor cores and the softmax, as the forward kernel; the codes are
-// read once an item, an eighth of the bytes of a bf16 cache.
+// Bound: the tensor cores, the softmax and putting K and V together share the
+// SM about evenly; the codes are read once an item, a quarter of the bytes of a
+// bf16 cache.  Two requests of 1000 queries, on 16384 and 3000 keys, H=32/8
+// d=128 (301 GFLOP): 428 us, 703 TFLOP/s; 4096 queries on 16384 keys 866
+// TFLOP/s.  Kept steps, whole calls: probabilities of a whole row held in
+// registers 929 us; 32 columns at a time 492; K and V by a group of four warps
+// each 450 (as two copies of the code 597: the instruction cache); one copy of
+// the column code 442; the join told what to do 435.  Without the exponentials
+// the call takes 391 us, without putting tiles together 431 of 489 (before the
+// second group), with neither and no softmax arithmetic 294: the rest is the
+// MMAs and the hand-overs between the warps.
 #pragma once
 
 #include "kv4_attend.cuh"
@@ -185,7 +193,7 @@ struct PutFactors {
 
 // The four warps that put K (`value`: V) tiles together from their codes, one
 // key a thread.  One code for both: as two, it and the softmax did not stay in
-// the instruction cache (MEASURED).  A key's data comes in steps so that no latency shows: its page
+// the instruction cache (450 -> 597 us).  A key's data comes in steps so that no latency shows: its page
 // two tiles ahead, its parameters a tile ahead, its codes as soon as the last
 // tile's are used.  The K warps read V's parameters too and say how large both
 // tiles' values are.

@@ -6,6 +6,9 @@
  *   O = softmax(scale * Q K^T) V                        (forward)
  *   dQ, dK, dV = gradients of sum(dO * O)               (backward)
  *
+ * and the operators of a serving step in front of it and over a paged key/value
+ * cache held in 4 bits: fa_rotary (and its gradient, for training) and fa_kv4_*.
+ *
  * Sources for the operations (page title, then section):
  *   - "FlashAttention为什么更快更省显存" (hi-bin.com lesson 16), opening formula:
  *     Attention(Q,K,V) = softmax(QK^T / sqrt(d_k)) V; section 把整张表改为分块计算:
@@ -21,7 +24,7 @@
  *   - "FlashAttention 为什么能节省显存并提速,是否改变注意力结果?" (mianstack.com
  *     q-0277), section 难点在于分块后softmax如何归一: the (m, l, u) merge rule.
  *
- * Layout (all calls): Q, K, V, O, dO, dQ, dK, dV are bf16 tensors of shape
+ * Layout (fa_fwd* and fa_bwd*; the others say theirs): Q, K, V, O, dO, dQ, dK, dV are bf16 tensors of shape
  * [B, H, N, d], row-major and contiguous (d innermost).  LSE is fp32 [B, H, N]:
  * the natural-log logsumexp of each row of scale * Q K^T over its unmasked
  * keys.  Query and key sequence lengths are equal (N).  d must be 64 or 128.
@@ -339,10 +342,17 @@ FA_API fa_status fa_kv4_gather(const void* cache, const long long* slots, void* 
  * it only chooses the kernel and sizes the workspace (larger requests are
  * still right).  Rows of q past cu_tokens[requests] are not touched.
  * Deterministic: the same arguments give the same bits.
+ * Precision: up to 47 rows a kv head (max_tokens * heads / kv_heads; 79 at
+ * d = 64) the scores are those of the cached values to 32 bits; above, keys and
+ * values go through fp16 (2^-12 of themselves on average).  P is fp16, O and
+ * the statistics 32 bits, O is rounded once.
+ * A cached key or value that is no number (see fa_kv4_append) makes the rows
+ * that see it NaN, in its 64 channels or in all, and no other row.
  *   workspace : fa_kv4_attention_workspace_size bytes, 16-byte aligned,
  *               contents on entry irrelevant.
  * A page index outside the cache is reported as FA_ERR_PAGE by
- * fa_check_device_error; its keys count as absent.
+ * fa_check_device_error; its keys count as absent.  Calls that may overlap (two
+ * streams, two replayed graphs) need a workspace each, as all calls here.
  */
 FA_API size_t fa_kv4_attention_workspace_size(int heads, int kv_heads, int d, int max_tokens);
 FA_API fa_status fa_kv4_attention(const void* q, const void* cache, const int* block_table,

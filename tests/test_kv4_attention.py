@@ -146,6 +146,22 @@ def test_long_and_many(d, H, G, R):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("heads", [1, 64])
+def test_a_long_context_keeps_its_small_output(heads):
+    """Half a million keys of nearly equal weight: O is their values' mean, two hundred
+    times smaller than they are, and still off by little more than its rounding (bf16
+    2^-8 at most, 2^-9.2 in root mean square; P in fp16 adds at most 2^-11 of 15 s a
+    key, of either sign: below 2^-11 of O)."""
+    c = Case(64, heads, 1, 64, [500_000], [1], seed=50, q_mult=0.25)
+    o, _ = fa.kv4_attention(c.q, c.cache, c.table, c.lens, c.cu, max_tokens=1)
+    tiles = c.cache[c.table[0, :-(-500_000 // 64)].long(), 0].reshape(-1, 18 * 64)
+    k, v, _, _ = (x[:500_000] for x in ref.read_tiles(tiles, 64))
+    w = torch.softmax(c.q[0].double() @ k.T / 8.0, -1) @ v
+    off = float((o[0].double() - w).norm() / w.norm())
+    assert off <= 2.0 ** -9, off
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("scale", [0.0, -0.09, 3.0])
 @pytest.mark.parametrize("q_mult", [1.0, 2.0 ** -40, 2.0 ** 30])
 def test_scales_and_sizes_of_q(scale, q_mult):
@@ -384,6 +400,41 @@ def test_two_streams_and_a_replayed_graph():
         graph.replay()
         c.compare(out, lse, True, 128 ** -0.5)
     fa.check_device_error()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [1, 40])
+def test_what_a_call_on_another_stream_allocates_stays_its_own(new):
+    """The call runs on a side stream that is still busy; memory it allocated itself
+    (the workspace, here at once free again) is not handed out meanwhile."""
+    c = Case(128, 8, 2, 16, [4000, 900], [new, new], seed=41)
+    kw = dict(max_tokens=new)
+    want = fa.kv4_attention(c.q, c.cache, c.table, c.lens, c.cu, **kw)
+    size = fa.kv4_attention_workspace_size(8, 2, 128, new)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(2_000_000)
+        got = fa.kv4_attention(c.q, c.cache, c.table, c.lens, c.cu, stream=side, **kw)
+        junk = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(3)]
+        for _ in range(20):
+            for j in junk:
+                j.fill_(255)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        del junk
+
+
+@pytest.mark.gpu
+def test_axes_of_length_one_may_have_any_stride():
+    c = Case(128, 4, 1, 16, [50], [1], seed=42)
+    flat = torch.zeros(4 * 128 + 64, dtype=torch.bfloat16, device="cuda")
+    q = flat.as_strided((1, 4, 128), (3, 128, 1))
+    q.copy_(c.q)
+    want = fa.kv4_attention(c.q, c.cache, c.table, c.lens, c.cu, max_tokens=1)
+    got = fa.kv4_attention(q, c.cache, c.table, c.lens, c.cu, max_tokens=1)
+    assert torch.equal(got[0], want[0])
 
 
 @pytest.mark.gpu
