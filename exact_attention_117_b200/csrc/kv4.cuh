@@ -151,10 +151,12 @@ __device__ __forceinline__ float kv4_scale(float span) {
 // lowest = the minimum (a bf16 already), scale = the smallest bf16 with 15
 // scale >= span, n = floor((x - lowest) / scale + 1/2).  The comparisons are
 // exact.  With dist = x - lowest rounded down and a reciprocal a little too
-// small, n0 = dist * reciprocal to the nearest is n or n - 1; it is n - 1 just
-// where dist - n0 scale, rounded down, is not below scale / 2: every border
-// (n0 + 1/2) scale is a 32-bit number, and rounding down moves no number across
-// it.  Four codes are packed as one exact 32-bit float.
+// large, n0 = dist * reciprocal to the nearest is n or, once in 10^5, n + 1; it is
+// n + 1 just where dist - n0 scale, rounded down, is below -scale / 2: every
+// border (n0 - 1/2) scale is a 32-bit number, and rounding down moves no number
+// across it.  Only the least of these differences is looked at, and a thread that
+// finds one too low corrects its codes.  Four codes are packed as one exact
+// 32-bit float.
 // A group with an infinity, a NaN or a span beyond the largest float reads back
 // as NaN.
 //
@@ -197,17 +199,25 @@ __device__ __forceinline__ void append_words(const Kv4StoreParams& p, const Stor
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] *= 0x1p100f;
   }
-  // (scale 0: the products by a zero reciprocal leave every code 0, and half a
-  // step of infinity leaves it there)
-  const float inv = scale > 0.f ? __fdividef(1.f - 0x1p-20f, scale) : 0.f;
-  const float half = scale > 0.f ? 0.5f * scale : INFINITY;
-  float four[4] = {0.f, 0.f, 0.f, 0.f};
+  // (scale 0: the products by a zero reciprocal leave every code 0)
+  const float inv = scale > 0.f ? __fdividef(1.f + 0x1p-20f, scale) : 0.f;
+  const float half = 0.5f * scale;
+  float four[4] = {0.f, 0.f, 0.f, 0.f}, least_left = 0.f;
 #pragma unroll
   for (int i = 15; i >= 0; --i) {
     const float dist = __fsub_rd(x[i], lo);
-    float n = fmaf(dist, inv, 0x1p23f) - 0x1p23f;  // to the nearest whole number
-    if (__fmaf_rd(-n, scale, dist) >= half) n += 1.f;
+    const float n = fmaf(dist, inv, 0x1p23f) - 0x1p23f;  // to the nearest whole number
+    least_left = fminf(least_left, __fmaf_rd(-n, scale, dist));
     four[i >> 2] = fmaf(four[i >> 2], 16.f, n);
+  }
+  if (least_left < -half) {
+#pragma unroll
+    for (int i = 15; i >= 0; --i) {
+      const float dist = __fsub_rd(x[i], lo);
+      const float n = fmaf(dist, inv, 0x1p23f) - 0x1p23f;
+      if (__fmaf_rd(-n, scale, dist) < -half)
+        four[i >> 2] -= static_cast<float>(1 << (4 * (i & 3)));
+    }
   }
   // 2^23 + a whole number below 2^16: its bits are the number's
   uint32_t code[2];

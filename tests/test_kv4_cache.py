@@ -258,6 +258,26 @@ def test_append_borders_and_odd_values():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lift", [0, -100])
+def test_append_values_a_hair_from_a_border(lift):
+    """Tiny values in a group whose lowest is a whole border below 0: their distances
+    from it are that border give or take less than 32 bits hold."""
+    x = torch.zeros(64, dtype=torch.float64)
+    x[0], x[1] = -2.875, 0.875  # scale 1/4; 0 is the border 11 1/2 steps above the lowest
+    tiny = [2.0 ** -e for e in (10, 18, 20, 21, 22, 23, 30)]
+    x[2:9], x[9:16] = torch.tensor(tiny, dtype=torch.float64), -torch.tensor(tiny, dtype=torch.float64)
+    x = (x * 2.0 ** lift).bfloat16().reshape(1, 1, 64).cuda()
+    cache = fa.kv4_cache(1, 1, 16, 64)
+    slots = torch.zeros(1, dtype=torch.int64, device="cuda")
+    fa.kv4_append(x, x, cache, slots)
+    for got in fa.kv4_gather(cache, slots):
+        want = ref.dequantised(x)
+        assert torch.equal(got.double(), want)  # multiples of 1/8: exact in bf16
+        up = (got[0, 0].double() * 2.0 ** -lift + 2.875) / 0.25
+        assert up[2:9].tolist() == [12.0] * 7 and up[9:16].tolist() == [11.0] * 7
+
+
+@pytest.mark.gpu
 def test_append_skips_slots_outside_and_reads_zeros_there():
     H, d, page = 2, 128, 32
     cache = torch.randint(0, 255, (3, H, 2, 18 * d), device="cuda", dtype=torch.uint8)
