@@ -212,6 +212,13 @@ fa_status fa_rotary(const void* q, const void* k, void* q_out, void* k_out, int 
       (reinterpret_cast<uintptr_t>(positions) & (positions_64 ? 7u : 3u)))
     return FA_ERR_ALIGN;
   if (N == 0) return FA_OK;
+  // an output that is its input lies as the input does
+  const long long sizes[2][3] = {{B, q_heads, N}, {B, k_heads, N}};
+  for (int w = 0; w < (k_heads ? 2 : 1); ++w)
+    for (int i = 0; i < 3; ++i)
+      if (ptrs[2 * w] == ptrs[2 * w + 1] && sizes[w][i] > 1 &&
+          strides[6 * w + i] != strides[6 * w + 3 + i])
+        return FA_ERR_SHAPE;
   fa::RotaryParams p = {};
   p.x[0] = q;
   p.x[1] = k;

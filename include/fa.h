@@ -245,7 +245,7 @@ typedef enum { FA_BF16 = 0, FA_FP16 = 1, FA_FP32 = 2 } fa_dtype;
  *     y1 = A (x1 cos t - x2 sin t),  y2 = A (x2 cos t + x1 sin t),
  * t = p * inv_freq[i]; channels from rotary_dim on pass through.
  *   q, q_out : [B, q_heads, N, d];  k, k_out : [B, k_heads, N, d] (k_heads = 0:
- *              no second tensor).  An output may be its input.
+ *              no second tensor).  An output may be its input, strides and all.
  *   strides  : 12 element strides (batch, head, position) of q, q_out, k,
  *              k_out; the last axis is contiguous.
  *   positions: int32, or int64 if positions_64: entry b * position_stride + n
@@ -256,9 +256,9 @@ typedef enum { FA_BF16 = 0, FA_FP16 = 1, FA_FP32 = 2 } fa_dtype;
  *   amplitude : A.  inverse != 0 turns by -t: with the same A this is the
  *              gradient of the call (dq_out, dk_out in, dq, dk out).
  *   dtype    : FA_BF16, FA_FP16 or FA_FP32; products in 32 bits, one rounding.
- * N = 0 does nothing.  FA_ERR_SHAPE for an odd rotary_dim or one above d,
- * FA_ERR_ALIGN where an element (a pair, if interleaved) is not aligned to
- * its size.
+ * N = 0 does nothing.  FA_ERR_SHAPE for an odd rotary_dim or one above d, or an
+ * output at its input's address with other strides, FA_ERR_ALIGN where an
+ * element (a pair, if interleaved) is not aligned to its size.
  */
 FA_API fa_status fa_rotary(const void* q, const void* k, void* q_out, void* k_out, int B,
                            int q_heads, int k_heads, int N, int d, const long long* strides,

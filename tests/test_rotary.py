@@ -35,6 +35,17 @@ def test_refusals():
     assert _raw(N=0) == 0 and _raw(N=0, q=None, qo=None, pos=None) == 0
 
 
+def test_an_output_at_its_inputs_address_lies_as_it_does():
+    from exact_attention_117_b200 import build
+    build.build()
+    q, other = [1024, 256, 64], [1024, 64, 256]
+    k = [512, 256, 64]
+    heads = dict(Hq=4, Hk=2, B=2, N=4)
+    assert _raw(strides=q + other + k + k, **heads) == 2
+    assert _raw(strides=q + q + k + [512, 64, 128], **heads) == 2
+    assert _raw(strides=q + other + k + k, Hq=4, Hk=2, B=2, N=0) == 0
+
+
 def test_binding_refuses():
     x = torch.zeros(1, 2, 3, 64, dtype=torch.bfloat16)
     f = torch.ones(32, dtype=torch.float64)
