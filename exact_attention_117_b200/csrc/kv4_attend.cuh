@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, (Kv4AttendLayout<D, NT>::kCtas
       if (lane < kBT && tile < tile_end) {
         const int page = p.page_tiles(tile), id = table[page];
         if (static_cast<unsigned>(id) < static_cast<unsigned>(p.pages))
-          from = id * page_bytes + (tile - page * tiles_per_page) * T::kBytes;
+          from = id * page_bytes + static_cast<long long>(tile - page * tiles_per_page) * T::kBytes;
         else
           atomicOr(&g_error_word, kErrBadPage);
       }

@@ -438,6 +438,28 @@ def test_axes_of_length_one_may_have_any_stride():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("new", [1, 64])
+def test_one_page_of_more_than_2_to_the_31_bytes(new):
+    """A key far behind in a page of its own takes all the weight (its score is
+    above 180, all others are 0): O is its value."""
+    page, far = 1 << 24, (1 << 24) - 33
+    cache = fa.kv4_cache(1, 1, page, 128)
+    k = torch.full((1, 1, 128), 4.0, device="cuda").bfloat16()
+    v = torch.randn(1, 1, 128, device="cuda").bfloat16()
+    fa.kv4_append(k, v, cache, torch.tensor([far], device="cuda"))
+    q = k.expand(new, 1, 128).contiguous()
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    o, lse = fa.kv4_attention(q, cache, ints(0)[None], ints(page), ints(0, new), max_tokens=new,
+                              causal=False)
+    _, want = fa.kv4_gather(cache, torch.tensor([far], device="cuda"))
+    # bf16's rounding of the value and of O, P's and V's to fp16
+    assert torch.allclose(o.float(), want[0].float().expand(new, 1, 128).reshape(o.shape),
+                          rtol=2.0 ** -7 + 2.0 ** -10, atol=2.0 ** -9 * float(v.abs().max()))
+    assert torch.allclose(lse, torch.full_like(lse, 128 * 16 / math.sqrt(128)), rtol=1e-4)
+    fa.check_device_error()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("d,H,G,page,interleaved", [(128, 8, 2, 64, False), (64, 6, 3, 16, True)])
 def test_serving_steps(d, H, G, page, interleaved):
     """Requests that come, grow and go: each step plans its pages, turns q and k,
