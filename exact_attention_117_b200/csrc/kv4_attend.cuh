@@ -44,6 +44,7 @@ struct Kv4AttendParams {
   long long q_st, q_sh, o_st, o_sh;  // strides in elements
   long long table_stride;
   int requests, heads, kv_heads, group, tokens, pages, page_size, width;
+  int lead;               // units of a job before those of its keys
   FastDiv page_tiles, by_group;  // 16-key tiles of a page, heads of a group
   float scale_log2;
   int causal, is_half;
@@ -53,12 +54,13 @@ struct Kv4AttendParams {
 constexpr int kKv4Warps = 4;
 
 // ------------------------------------------------------------ the work's order
-// Units: (request, tile of ROWS rows, kv head, UNIT keys), keys innermost; a row
-// tile has as many as its last row's visible keys fill (one if it sees none, so
-// that its zeros are written).  Each CTA takes an equal, contiguous range of
-// them, and so reads the same share of the cache whatever the lengths are.  A
-// (request, row tile, head) that a CTA's range cuts is left as partial results,
-// which the combine kernel joins.
+// Jobs: (request, tile of ROWS rows, kv head).  A job's units are first p.lead
+// that stand for what it costs to begin and end one (q, the first keys'
+// latency, the output), then one for each UNIT keys that its last row sees (in
+// all at least one, so that a row that sees none gets its zeros).  Each CTA takes
+// an equal, contiguous range of the units, and so an equal share of the time
+// whatever the lengths are.  A job that a CTA's range cuts is left as partial
+// results, which the combine kernel joins.
 struct Kv4Req {
   int first, n, len, rows;  // first query, queries, keys, rows (queries * group)
 };
@@ -79,7 +81,7 @@ __device__ __forceinline__ int kv4_sees(const Kv4AttendParams& p, const Kv4Req& 
 template <int ROWS, int UNIT>
 __device__ __forceinline__ int kv4_tile_units(const Kv4AttendParams& p, const Kv4Req& r, int tile) {
   const int last = min((tile + 1) * ROWS, r.rows) - 1;
-  return max(1, (kv4_sees(p, r, last) + UNIT - 1) / UNIT);
+  return max(1, p.lead + (kv4_sees(p, r, last) + UNIT - 1) / UNIT);
 }
 template <int ROWS, int UNIT>
 __device__ __forceinline__ long long kv4_units(const Kv4AttendParams& p, const Kv4Req& r) {
@@ -647,8 +649,8 @@ __global__ void __launch_bounds__(kKv4Warps * 32, (Kv4AttendLayout<D, NT>::kCtas
 
     // ---- fill the ring; pages of the block after next are looked up an
     // iteration ahead of their copy
-    const int tile_end = min(c1 * (L::kUnit / 16), (any_sees + 15) / 16);
-    const int blk0 = c0 * kKv4Warps + warp;
+    const int tile_end = min(max(c1 - p.lead, 0) * (L::kUnit / 16), (any_sees + 15) / 16);
+    const int blk0 = max(c0 - p.lead, 0) * kKv4Warps + warp;
     const int n_blk = max(0, ((tile_end + kBT - 1) / kBT - blk0 + kKv4Warps - 1) / kKv4Warps);
     const int* table = p.table + b * p.table_stride;
     const uint8_t* head_base = p.cache + static_cast<long long>(h) * tiles_per_page * T::kBytes;

@@ -124,10 +124,10 @@ __device__ __forceinline__ ChunkPiece chunk_piece(const Kv4AttendParams& p,
   c.h = w.h;
   c.row0 = w.tile * kChunkRows;
   c.rows = min(kChunkRows, w.rq.rows - c.row0);
-  c.k0 = w.c0 * (kChunkUnit / 128);
+  c.k0 = max(w.c0 - p.lead, 0) * (kChunkUnit / 128);
   c.whole = w.c0 == 0 && units == w.units;
   c.head_cut = w.c0 > 0;
-  const int end = c.k0 + units * (kChunkUnit / 128);
+  const int end = max(w.c0 + units - p.lead, 0) * (kChunkUnit / 128);
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int last = min(128 * (t + 1), c.rows) - 1;

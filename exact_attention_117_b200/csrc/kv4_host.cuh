@@ -130,8 +130,21 @@ fa_status launch_join(void (*kernel)(fa::Kv4AttendParams, int), int ctas, int ro
   return cudaLaunchKernelEx(&cfg, kernel, p, ctas) == cudaSuccess && launched() ? FA_OK : FA_ERR_CUDA;
 }
 
+// Leading units of a job (kv4_attend.cuh): two, about what a job costs besides its
+// keys.  us without / with them on one B200, d = 128, H=32/8: 64 requests of 200 to
+// 8192 keys 86 / 76, 256 of 100 to 2000 135 / 95, 16 of 100 to 8000 33.5 / 27.3,
+// 64 of 4096 71 / 71; chunks: 2 x 1000 queries on 16384 and 3000 keys 435 / 388, one
+// of 1000 queries 55 / 46.  With fewer jobs than CTAs one is enough, and where
+// they are far fewer hardly a CTA has more than one job to begin, and leading
+// units only take CTAs from the keys (one request of 4096 keys 13.3 / 14.1).
+int attend_lead(const fa::Kv4AttendParams& p, int rows, int ctas, bool chunk) {
+  const long long each = (static_cast<long long>(p.tokens) * p.group + p.requests - 1) / p.requests;
+  const long long jobs = (each + rows - 1) / rows * p.requests * p.kv_heads;
+  return jobs * 8 < ctas ? 0 : jobs < ctas && !chunk ? 1 : 2;
+}
+
 template <int D, int NT>
-fa_status launch_attend(const fa::Kv4AttendParams& p, cudaStream_t st) {
+fa_status launch_attend(fa::Kv4AttendParams p, cudaStream_t st) {
   using L = fa::Kv4AttendLayout<D, NT>;
   static bool attr_set[kMaxDevices] = {};
   int dev = 0;
@@ -141,6 +154,7 @@ fa_status launch_attend(const fa::Kv4AttendParams& p, cudaStream_t st) {
     attr_set[dev] = true;
   }
   const int ctas = sm_count(dev) * L::kCtas;
+  p.lead = attend_lead(p, L::kRows, ctas, false);
   {
     LaunchTimer timer(st, FA_KERNEL_KV4_ATTEND);
     fa::kv4_attend_kernel<D, NT><<<ctas, fa::kKv4Warps * 32, L::kBytes, st>>>(p);
@@ -150,7 +164,7 @@ fa_status launch_attend(const fa::Kv4AttendParams& p, cudaStream_t st) {
 }
 
 template <int D>
-fa_status launch_chunk(const fa::Kv4AttendParams& p, cudaStream_t st) {
+fa_status launch_chunk(fa::Kv4AttendParams p, cudaStream_t st) {
   using L = fa::Kv4ChunkLayout<D>;
   static bool attr_set[kMaxDevices] = {};
   int dev = 0;
@@ -160,6 +174,7 @@ fa_status launch_chunk(const fa::Kv4AttendParams& p, cudaStream_t st) {
     attr_set[dev] = true;
   }
   const int ctas = sm_count(dev);
+  p.lead = attend_lead(p, fa::kChunkRows, ctas, true);
   {
     LaunchTimer timer(st, FA_KERNEL_KV4_ATTEND);
     fa::kv4_chunk_kernel<D><<<ctas, fa::kChunkWarps * 32, L::kSmemAlloc, st>>>(p);
