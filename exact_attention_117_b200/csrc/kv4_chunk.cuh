@@ -72,8 +72,9 @@ struct Kv4ChunkLayout {
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColS = 0, kColO = 256;  // S: 128 columns a tile, O: D
   static constexpr int kPartFloats = kChunkRows * (D + 2);
-  // the block launches with 96 registers a thread
-  static constexpr uint32_t kRegsOther = 64, kRegsPut = 64, kRegsSoftmax = 144;
+  // the block launches with 96 registers a thread; the MMA warp needs them all
+  // (64 / 64 / 144: its spilled values hold it up, 368 -> 388 us; 96 / 72 / 120: 375)
+  static constexpr uint32_t kRegsOther = 96, kRegsPut = 64, kRegsSoftmax = 128;
   static_assert(128 * (kRegsOther + 2 * kRegsPut + 2 * kRegsSoftmax) <= 640 * 96, "register split");
 };
 
@@ -387,7 +388,7 @@ __global__ void __launch_bounds__(kChunkWarps * 32, 1)
   }
 
   if (warp < 4) {
-    setmaxnreg_dec<L::kRegsOther>();
+    setmaxnreg_dec<L::kRegsOther>();  // (says how many; they are the launch's)
     if (warp == 0 && any) {
       // ------------------------------------------------------------ MMA issuer
       constexpr uint32_t id_s = idesc_f16_f32(128, 128, false);
