@@ -1051,7 +1051,7 @@ def main():
     ap.add_argument("--sweep", choices=["all", "c5", "splitkv", "kv_outer", "bwd", "kv4"], default=None,
                     help="supplementary per-case measurements instead of the headline line")
     ap.add_argument("--once", action="store_true",
-                    help="with --sweep c5, kv_outer or bwd: run the cases once, untimed (for ncu)")
+                    help="with --sweep c5, kv_outer, bwd or kv4: run the cases once, untimed (for ncu)")
     ap.add_argument("--case", default=None,
                     help="with --sweep c5: only this workload (e.g. c5_d64_n4096)")
     ap.add_argument("--traffic", action="store_true",

@@ -133,7 +133,7 @@ fa_status launch_join(void (*kernel)(fa::Kv4AttendParams, int), int ctas, int ro
 // Leading units of a job (kv4_attend.cuh): two, about what a job costs besides its
 // keys.  us without / with them on one B200, d = 128, H=32/8: 64 requests of 200 to
 // 8192 keys 86 / 76, 256 of 100 to 2000 135 / 95, 16 of 100 to 8000 33.5 / 27.3,
-// 64 of 4096 71 / 71; chunks: 2 x 1000 queries on 16384 and 3000 keys 435 / 388, one
+// 64 of 4096 71 / 71; chunks: 1000 queries on 16384 keys and on 3000 435 / 388, one
 // of 1000 queries 55 / 46.  With fewer jobs than CTAs one is enough, and where
 // they are far fewer hardly a CTA has more than one job to begin, and leading
 // units only take CTAs from the keys (one request of 4096 keys 13.3 / 14.1).
