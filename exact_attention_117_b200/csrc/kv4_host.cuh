@@ -32,17 +32,19 @@ fa_status rotary_typed(fa::RotaryParams p, int B, bool interleaved, cudaStream_t
   const int vec = wide ? kV : interleaved ? 2 : 1;
   const bool in_place = p.x[0] == p.y[0] && (!p.heads[1] || p.x[1] == p.y[1]);
   p.chunks = (interleaved ? p.rot : p.rot / 2) / vec + (in_place ? 0 : (p.d - p.rot) / vec);
-  // A block: up to 8 positions (512 sines, 256 vectors of a head), and as many
-  // heads as give each thread 8 vectors (so that sines are computed once for
-  // them) where that still fills the GPU, one otherwise.
+  // A thread takes 1, 2, 4 or 8 vectors, as many as leave three blocks an SM, and
+  // a block as many positions (512 sines, 256 vectors of a head at most), so that
+  // sines are computed once for several heads and a block's latencies count once
+  // for several vectors (2048 tokens of 40 heads, d = 128, one vector a thread: 28 us).
   const int heads = p.heads[0] + p.heads[1], pairs = p.rot / 2;
   const long long all = static_cast<long long>(B) * p.n * heads * p.chunks;
-  const bool many = all >= 8LL * fa::kRotaryThreads * 148 * 3;
-  p.block_pos = std::max(1, std::min({many ? 8 : 1, fa::kRotaryPairs / pairs,
-                                      fa::kRotaryThreads / p.chunks, p.n}));
+  int per = 8;
+  while (per > 1 && all < per * (fa::kRotaryThreads * 148LL * 3)) per /= 2;
+  p.block_pos = std::max(1, std::min({per, fa::kRotaryPairs / pairs, fa::kRotaryThreads / p.chunks, p.n}));
   p.block_rows = p.block_pos * p.chunks;
-  p.block_heads = std::min(heads, (many ? 8 : 1) * (fa::kRotaryThreads / p.block_rows));
+  p.block_heads = std::min(heads, per * (fa::kRotaryThreads / p.block_rows));
   p.head_groups = (heads + p.block_heads - 1) / p.block_heads;
+  p.block_heads = (heads + p.head_groups - 1) / p.head_groups;
   p.pos_blocks = (p.n + p.block_pos - 1) / p.block_pos;
   const long long blocks = static_cast<long long>(B) * p.pos_blocks * p.head_groups;
   if (blocks > 0x7fffffffLL) return FA_ERR_SHAPE;

@@ -146,6 +146,17 @@ def test_long_and_many(d, H, G, R):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d,H,G,new", [(128, 8, 4, 1), (64, 4, 2, 3), (128, 8, 2, 20), (64, 4, 1, 30)])
+def test_many_uneven_jobs(d, H, G, new):
+    """More jobs than CTAs, of unlike lengths and some without a key, so that ranges
+    begin and end anywhere in them."""
+    rng = random.Random(d + new)
+    lens = [rng.choice([0, 1, 5, 17, 255, 256, 257, 300, 900, 2000]) for _ in range(170)]
+    lens[40:44] = [6000, 0, 0, 0]
+    Case(d, H, G, 16, lens, [rng.choice([0, 1, new]) for _ in lens], seed=new).check(most=new)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("heads", [1, 64])
 def test_a_long_context_keeps_its_small_output(heads):
     """Half a million keys of nearly equal weight: O is their values' mean, two hundred

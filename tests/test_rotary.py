@@ -108,6 +108,21 @@ def test_rotary_matches_definition(dtype, interleaved, d, rot, B, H, Hk, N):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("H,Hk,N", [(32, 8, 800), (32, 8, 2048), (5, 2, 8191), (1, 0, 70001)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_sizes_between_a_decode_step_and_a_training_batch(H, Hk, N, interleaved):
+    f, a = fa.rotary_frequencies(128)
+    g = torch.Generator(device="cuda").manual_seed(N)
+    q = torch.randn(1, H, N, 128, generator=g, device="cuda").bfloat16()
+    k = torch.randn(1, Hk, N, 128, generator=g, device="cuda").bfloat16() if Hk else None
+    pos = torch.randint(0, 100000, (N,), generator=g, device="cuda", dtype=torch.int32)
+    y, z = fa.rotary(q, k, pos, f, interleaved)
+    _check(y, q, ref.rotary(q, pos, f, interleaved, a), "q")
+    if Hk:
+        _check(z, k, ref.rotary(k, pos, f, interleaved, a), "k")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_far_positions_keep_their_phase(interleaved):
     q = torch.randn(1, 2, 6, 128, device="cuda")
