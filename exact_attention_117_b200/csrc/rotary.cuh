@@ -12,8 +12,8 @@
 // in 32 bits.  The products are 32-bit; the result is rounded once.
 //
 // Bound: every channel is read once and written once; the issue slots are half
-// taken.  B=2 H=16 N=4096 d=128, queries and keys (134 MB): 24.5 us, 5.5 TB/s; a
-// decode step of 8 tokens 3.2 us, a launch.
+// taken.  B=2 H=16 N=4096 d=128, queries and keys (134 MB): 24.1 us, 5.6 TB/s; a
+// decode step of 8 tokens 2.8 us, a launch.
 //
 // A block takes a few positions and a range of heads.  Its threads first compute
 // each (position, pair)'s sine and cosine once, into shared memory, with their
