@@ -12,9 +12,10 @@
 // Codes enter as fp16 subnormal numbers, exactly.  q enters as fp16 after an
 // exact scaling of each row by a power of two (its largest element near fp16's
 // largest), so a bf16 or fp16 q keeps all its bits down to 2^-24 of the row's
-// largest.  P s enters as fp16 relative to a power of two above the largest s
-// seen: 11 bits, against the 8 of a bf16 P.  Scores, softmax statistics and O
-// are fp32.
+// largest.  P s enters as fp16 times a power of two of its row and 64-channel
+// group, by the largest P s that the row has met: 11 bits, against the 8 of a
+// bf16 P, and none lost to a large token without weight, to another group or to
+// a token that the row does not see.  Scores, softmax statistics and O are fp32.
 //
 // Rows: the queries of a request times the heads that share a kv head, in
 // tiles of 8 NT.  Transposed products (S^T = K q^T, O^T = V^T P^T) put tokens
@@ -221,6 +222,17 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+// Two 32-bit operations in one instruction.
+__device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
 // Codes 0..7 of a word as four fp16 pairs: (0, 4), (1, 5), (2, 6), (3, 7).  Four
 // bits at the bottom of an fp16 are the subnormal number n 2^-24, four bits
 // higher 16 n 2^-24: exact operands of the matrix instructions without any
@@ -379,14 +391,31 @@ __device__ __forceinline__ void kv4_rows(const Kv4AttendParams& p, const Kv4Req&
   factor = __uint_as_float(static_cast<uint32_t>(e + 10) << 23) * p.scale_log2;
 }
 
-// Running state of a warp's rows (columns 2t, 2t + 1 of each row tile).
+// Running state of a warp's rows (columns 2t, 2t + 1 of each row tile).  A row's
+// state follows from the keys that the row sees alone: what moves for one row
+// moves for no other, so a row's bits do not depend on tokens hidden from it.
 template <int D, int NT>
 struct Kv4State {
-  float acc[D / 64][4][NT][4];  // O^T 2^-24 vinv, odd channels times 16
+  float acc[D / 64][4][NT][4];  // O^T 2^-34 w, odd channels times 16
   float lo_sum[NT][D / 64][2];  // sum of P times V's lowest values
   float l[NT][2], m[NT][2];
-  float vinv;                   // a power of two: the largest scale of V times it is below 8
+  uint32_t w[NT];  // byte 2 group + r: the unit w = 2^(2 byte - 127) of P s 2^-10; byte 0: w = 0
 };
+__device__ __forceinline__ float kv4_unit(uint32_t w, int gp, int r) {
+  return __uint_as_float(__byte_perm(w, 0, 0x444 | (2 * gp + r) << 12));
+}
+// The unit that brings `big` to [8, 32), and the least that a unit was found for.
+__device__ __forceinline__ uint32_t kv4_unit_byte(float big) {
+  return min(max((258 - static_cast<int>(__float_as_uint(big) >> 23)) >> 1, 2), 126);
+}
+// One unit over another, 0 where that one is 0; at most 2^126.
+__device__ __forceinline__ float kv4_unit_ratio(uint32_t to, uint32_t from) {
+  const int steps = static_cast<int>(to) - static_cast<int>(from);
+  return from == 0 || steps < -63 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + 2 * min(steps, 63)) << 23);
+}
+__device__ __forceinline__ float kv4_unit_least(float unit) {
+  return unit == 0.f ? 0.f : __uint_as_float(0x80800000u - __float_as_uint(unit));  // 8 / unit
+}
 
 // A lane's places in a tile: K code words of its two rows' first, their
 // parameters, V code words of its four tokens' first.
@@ -457,6 +486,8 @@ __device__ __forceinline__ void kv4_tiles(const uint8_t* tile, const Kv4Lane<D>&
   int key[kTok];
   float vs[kTok][kGroups], vl[kTok][kGroups], x[NT][2 * kTok], y[NT][2 * kTok];
   float most = 0.f;
+  // (s times 2^-10, so that its product with P below 2^8 is finite for every s;
+  // negative for the tiles taken from above)
 #pragma unroll
   for (int i = 0; i < kTok; ++i) {
     key[i] = key0 + kv4_tau(lane >> 2) + 8 * i;
@@ -464,10 +495,9 @@ __device__ __forceinline__ void kv4_tiles(const uint8_t* tile, const Kv4Lane<D>&
 #pragma unroll
     for (int gp = 0; gp < kGroups; ++gp) {
       const float s_v = bf16_lo(vp[i][gp]), lowest = bf16_hi(vp[i][gp]);
-      vs[i][gp] = gone ? 0.f : s_v * st.vinv;
+      vs[i][gp] = gone ? 0.f : s_v * (odd(i >> 1) ? -0x1p-10f : 0x1p-10f);
       vl[i][gp] = gone ? 0.f : odd(i >> 1) ? fmaf(15.f, s_v, lowest) : lowest;
     }
-    most = kGroups == 2 ? fmax3(vs[i][0], vs[i][kGroups - 1], most) : fmaxf(vs[i][0], most);
   }
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -487,29 +517,11 @@ __device__ __forceinline__ void kv4_tiles(const uint8_t* tile, const Kv4Lane<D>&
 #pragma unroll
     for (int c = 0; c < 2 * kTok; c += 2) most = fmax3(y[nt][c], y[nt][c + 1], most);
   }
-  // ---- the running reference moves only when a score passes it by 2^8 (or a
-  // scale of V passes its own): P stays below 2^8, far from fp16's largest, and
-  // most tiles need no reduction over lanes
-  if (__any_sync(0xffffffffu, most > 8.f)) {
-    float top = 0.f, vf = 1.f;
-#pragma unroll
-    for (int i = 0; i < kTok; ++i)
-#pragma unroll
-      for (int gp = 0; gp < kGroups; ++gp)
-        if (!kMasked || key[i] < any_sees) top = fmaxf(top, bf16_lo(vp[i][gp]));
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (st.vinv == 0.f || top * st.vinv > 8.f) {  // the largest to [4, 8)
-      const uint32_t e = min(max(__float_as_uint(top) >> 23, 2u), 254u);
-      const float next = __uint_as_float((256u - e) << 23);
-      vf = st.vinv == 0.f ? 0.f : next / st.vinv;
-      st.vinv = next;
-#pragma unroll
-      for (int i = 0; i < kTok; ++i)
-#pragma unroll
-        for (int gp = 0; gp < kGroups; ++gp)
-          vs[i][gp] = kMasked && key[i] >= any_sees ? 0.f : bf16_lo(vp[i][gp]) * next;
-    }
+  // ---- a row's running reference moves only when one of its scores passes it by
+  // 2^8: most tiles need no reduction over lanes
+  const bool moves = __any_sync(0xffffffffu, most > 8.f);
+  float fall[NT][2];  // what P of the keys so far is multiplied by
+  if (moves) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -520,11 +532,10 @@ __device__ __forceinline__ void kv4_tiles(const uint8_t* tile, const Kv4Lane<D>&
           if (!kMasked || key[c >> 1] < lim[nt][r]) hi = fmaxf(hi, x[nt][c]);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        float f = 1.f;
-        if (hi > st.m[nt][r]) {
-          f = ex2_approx(st.m[nt][r] - hi);
-          st.m[nt][r] = hi;
-        }
+        const bool over = hi - st.m[nt][r] > 8.f;
+        const float f = over ? ex2_approx(st.m[nt][r] - hi) : 1.f;
+        st.m[nt][r] = over ? hi : st.m[nt][r];
+        fall[nt][r] = f;
         st.l[nt][r] *= f;
 #pragma unroll
         for (int gp = 0; gp < kGroups; ++gp) st.lo_sum[nt][gp][r] *= f;
@@ -532,8 +543,8 @@ __device__ __forceinline__ void kv4_tiles(const uint8_t* tile, const Kv4Lane<D>&
         for (int j = 0; j < kVW; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            st.acc[j][i][nt][r] *= f * vf;
-            st.acc[j][i][nt][r + 2] *= f * vf;
+            st.acc[j][i][nt][r] *= f;
+            st.acc[j][i][nt][r + 2] *= f;
           }
 #pragma unroll
         for (int c = r; c < 2 * kTok; c += 2) {
@@ -552,20 +563,59 @@ __device__ __forceinline__ void kv4_tiles(const uint8_t* tile, const Kv4Lane<D>&
       e[c] = ex2_approx(y[nt][c]);
       st.l[nt][c & 1] += e[c];
     }
+    // The fragments of P s, a second time where a group's unit moves: with its row's
+    // reference, and where a P s would pass 2^15 (fp16 ends below 2^16).
+#pragma unroll 1
+    for (int pass = 0;; ++pass) {
+      float top = 0.f;
+#pragma unroll
+      for (int gp = 0; gp < kGroups; ++gp) {
+        const float2 unit = make_float2(kv4_unit(st.w[nt], gp, 0), kv4_unit(st.w[nt], gp, 1));
+#pragma unroll
+        for (int i = 0; i < kTok; ++i) {
+          float2 v = mul_f32x2(make_float2(e[2 * i] * vs[i][gp], e[2 * i + 1] * vs[i][gp]), unit);
+          if (kMasked && key[i] >= lim[nt][0]) v.x = 0.f;
+          if (kMasked && key[i] >= lim[nt][1]) v.y = 0.f;
+          top = fmax3(fabsf(v.x), fabsf(v.y), top);
+          pb[i >> 1][nt][gp][i & 1] = transpose8(pack_f16x2(v.x, v.y));
+        }
+      }
+      if (pass == 1 || !__any_sync(0xffffffffu, moves || top > 32768.f)) break;
+      uint32_t next = st.w[nt];
+#pragma unroll
+      for (int gp = 0; gp < kGroups; ++gp)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float hi = 0.f;
+#pragma unroll
+          for (int c = r; c < 2 * kTok; c += 2)
+            if (!kMasked || key[c >> 1] < lim[nt][r]) hi = fmaxf(hi, fabsf(e[c] * vs[c >> 1][gp]));
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+          const float old = kv4_unit(st.w[nt], gp, r), was = moves ? fall[nt][r] : 1.f;
+          if (was == 1.f && !(hi * old > 32768.f)) continue;
+          const uint32_t byte = kv4_unit_byte(fmaxf(kv4_unit_least(old) * was, hi));
+          const int at = 8 * (2 * gp + r);
+          const float f = kv4_unit_ratio(byte, st.w[nt] >> at & 0xffu);
+          next = (next & ~(0xffu << at)) | byte << at;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            st.acc[gp][i][nt][r] *= f;
+            st.acc[gp][i][nt][r + 2] *= f;
+          }
+        }
+      st.w[nt] = next;
+    }
 #pragma unroll
     for (int gp = 0; gp < kGroups; ++gp)
 #pragma unroll
-      for (int i = 0; i < kTok; ++i) {
-        float pv[2];
+      for (int i = 0; i < kTok; ++i)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const bool hidden = kMasked && key[i] >= lim[nt][r];
-          pv[r] = hidden ? 0.f : e[2 * i + r] * (odd(i >> 1) ? -vs[i][gp] : vs[i][gp]);
           st.lo_sum[nt][gp][r] = hidden ? st.lo_sum[nt][gp][r]
                                         : fmaf(e[2 * i + r], vl[i][gp], st.lo_sum[nt][gp][r]);
         }
-        pb[i >> 1][nt][gp][i & 1] = transpose8(pack_f16x2(pv[0], pv[1]));
-      }
   }
   // ---- O^T += V^T P^T
 #pragma unroll
@@ -779,7 +829,6 @@ __global__ void __launch_bounds__(kKv4Warps * 32, (Kv4AttendLayout<D, NT>::kCtas
     if (*abort_flag) return;
 
     // ---- this warp's results to shared memory
-    const float vref = st.vinv == 0.f ? 0.f : 1.f / st.vinv;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -799,10 +848,11 @@ __global__ void __launch_bounds__(kKv4Warps * 32, (Kv4AttendLayout<D, NT>::kCtas
 #pragma unroll
         for (int j = 0; j < kVW; ++j) {
           float v[8];
+          const float up = 0.125f * kv4_unit_least(kv4_unit(st.w[nt], j, r));  // 1 / unit
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            v[2 * k] = fmaf(st.acc[j][k][nt][r] * 0x1p24f, vref, lo[j]);
-            v[2 * k + 1] = fmaf(st.acc[j][k][nt][r + 2] * 0x1p20f, vref, lo[j]);
+            v[2 * k] = fmaf(st.acc[j][k][nt][r] * 0x1p34f, up, lo[j]);
+            v[2 * k + 1] = fmaf(st.acc[j][k][nt][r + 2] * 0x1p30f, up, lo[j]);
           }
           *reinterpret_cast<float4*>(to + 64 * j + 8 * g) = make_float4(v[0], v[1], v[2], v[3]);
           *reinterpret_cast<float4*>(to + 64 * j + 8 * g + 4) = make_float4(v[4], v[5], v[6], v[7]);

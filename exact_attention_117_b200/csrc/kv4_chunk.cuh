@@ -151,16 +151,6 @@ __device__ __forceinline__ uint4 put_word(uint32_t w, uint32_t s24, uint32_t s20
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// Two 32-bit operations in one instruction.
-__device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
-  float2 r;
-  asm("{\n\t.reg .b64 x, y, w;\n\t"
-      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "mul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}\n"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
 __device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
   float2 r;
   asm("{\n\t.reg .b64 x, y, w;\n\t"
