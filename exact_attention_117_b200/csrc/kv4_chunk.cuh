@@ -8,13 +8,17 @@
 //
 // Operands.  Q rows enter as fp16 times a power of two that brings the row's
 // largest element near fp16's largest (exact for bf16 and fp16 input down to
-// 2^-24 of it).  K and V tiles are put together by four warps from the codes:
-// lowest + scale n in one fused multiply-add, rounded once to fp16, in units of
-// a power of two that is the tile's for K and the largest so far for V (O is
-// rescaled when it grows).  So a key or value is off by 2^-12 of itself, an
-// eighth of what a bf16 copy of the cache would be off, and the scores by
-// about 2^-12 of their terms' root mean square; P is fp16 as in kv4_attend.cuh,
-// statistics and O are fp32.  The channels of a 64-bit chunk of codes stay in
+// 2^-24 of it).  K and V tiles are put together by four warps each from the codes:
+// lowest, rounded to fp16, plus scale n in one fused multiply-add, in units of a
+// power of two that bring the largest value to [2^8, 2^9).  So a key or value is
+// off by at most 2^-11 of itself and of its group's lowest (a bf16 copy of the
+// cache: 2^-8 of itself), and those below 2^-22 of the largest by 2^-33 of it.
+// Whose largest: of the tile for K, of the keys so far for V (O is rescaled when
+// it grows), where every row of the item sees the whole tile; in the last tiles,
+// with keys that some rows do not see, each key has units of its own: the
+// score's columns are multiplied by K's, and P by V's over a unit of the row that
+// follows from the keys it sees.  So no bit of a row depends on a key hidden
+// from it.  P is fp16, statistics and O are fp32.  The channels of a 64-bit chunk of codes stay in
 // the order in which they come out of a word, (0, 4), (1, 5), (2, 6), (3, 7):
 // Q is laid out alike, and O's columns are put back in order when they leave.
 //
@@ -68,7 +72,7 @@ struct Kv4ChunkLayout {
   static constexpr int kOffAbort = kOffSlot + 4;
   static constexpr int kBytes = kOffAbort + 8;
   static constexpr int kSmemAlloc = kBytes + 1024;  // slack to align the base to 1 KiB
-  static_assert(kSmemAlloc + 1024 <= 232448, "shared memory budget");
+  static_assert(kSmemAlloc + 6144 <= 232448, "shared memory budget");
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColS = 0, kColO = 256;  // S: 128 columns a tile, O: D
   static constexpr int kPartFloats = kChunkRows * (D + 2);
@@ -140,14 +144,16 @@ __device__ __forceinline__ ChunkPiece chunk_piece(const Kv4AttendParams& p,
 }
 
 // 8 codes as fp16 lowest + scale n, pairs (0, 4), (1, 5), (2, 6), (3, 7).  The
-// codes are subnormal numbers n 2^-24 or 16 n 2^-24; s24 and s20 carry 2^24 and
-// 2^20 times the scale.
-__device__ __forceinline__ uint4 put_word(uint32_t w, uint32_t s24, uint32_t s20, uint32_t lo) {
+// codes are subnormal numbers n 2^-24 or 16 n 2^-24; a multiplication makes them
+// n 2^-9 (exactly), so that 2^9 scale is an fp16 number for values up to 2^9.
+__device__ __forceinline__ uint4 put_word(uint32_t w, uint32_t s9, uint32_t lo) {
   uint32_t c[4], r[4];
   codes_f16(w, c);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r[i]) : "r"(c[i]), "r"(i & 1 ? s20 : s24), "r"(lo));
+  for (int i = 0; i < 4; ++i) {
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(c[i]) : "r"(c[i]), "r"(i & 1 ? 0x68006800u : 0x78007800u));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r[i]) : "r"(c[i]), "r"(s9), "r"(lo));
+  }
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
@@ -162,22 +168,33 @@ __device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
 }
 
 // Shared memory of a CTA beside the tiles: what a key tile's factors are, by
-// tile number mod 4.  The K warps write a tile's place once K of the tile two
-// before has been multiplied: by then the softmax and the V warps have read
-// what the place held, four tiles before.
+// tile number mod 4.  The K warps write tile g's place after they have seen K of
+// tile g - 3 multiplied (the wait in front of tile g - 1's words).  Those products
+// are issued behind the arrivals that end the softmax of tile g - 4 and the V warps'
+// work on it, the last that read the place: with four places there is none to spare.
 struct ChunkShared {
   float k_up[4];          // K in the tile is K / k_up
   alignas(16) uint32_t absent[4][4];  // keys whose page lies outside the cache
+  alignas(16) float own_up[4][2][128];  // a key's units of K and V, times 2^-32, in a tile of own units
   int size[4][4][2];      // per K warp: largest exponent of K and V
 };
 
-// The factors of a key's codes: 2^24 and 2^20 scale, lowest, in its unit.
+// Units.  Exponents (with float's bias) are kept where unit, its reciprocal and
+// the unit times 2^-32 are normal numbers: values below 2^-86 count as small
+// parts of 2^-86.
+__device__ __forceinline__ int chunk_size(int exponent) { return min(max(exponent, 41), 254); }
+__device__ __forceinline__ float chunk_up(int size) { return __uint_as_float(static_cast<uint32_t>(size - 8) << 23); }
+__device__ __forceinline__ float chunk_down(int size) { return __uint_as_float(static_cast<uint32_t>(262 - size) << 23); }
+// Whether key tile `tile` has own units: some row of the item does not see all
+// of its keys (`sure`: what the first row sees).
+__device__ __forceinline__ bool chunk_own(int tile, int len, int sure) { return min(128 * tile + 128, len) > sure; }
+
+// The factors of a key's codes: 2^9 scale, lowest, in its unit.
 struct PutFactors {
-  uint32_t s24, s20, lo;
-  __device__ __forceinline__ PutFactors(uint32_t par, float unit) {
-    const float s = bf16_lo(par) * unit, l = bf16_hi(par) * unit;
-    s24 = pack_f16x2(s * 0x1p24f, s * 0x1p24f);
-    s20 = pack_f16x2(s * 0x1p20f, s * 0x1p20f);
+  uint32_t s9, lo;
+  __device__ __forceinline__ PutFactors(uint32_t par, float down) {
+    const float s = bf16_lo(par) * down * 512.f, l = bf16_hi(par) * down;
+    s9 = pack_f16x2(s, s);
     lo = pack_f16x2(l, l);
   }
 };
@@ -219,7 +236,8 @@ __device__ __forceinline__ void chunk_put(bool value, const Kv4AttendParams& p, 
   };
   // Keys from `sure` on are hidden from some rows: 0 times a value that is no
   // finite number would reach them, so there a key that has one gets values 0
-  // and a score of NaN instead, for the rows that see it.
+  // and a score of NaN instead, for the rows that see it.  (The largest scale that
+  // values of 32 bits have is below 2^125.)
   auto fetch_par = [&](const ChunkPiece& c, int sure, int j) {
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) kp[i] = vp[i] = 0;
@@ -229,7 +247,7 @@ __device__ __forceinline__ void chunk_put(bool value, const Kv4AttendParams& p, 
     if ((c.k0 + j) * 128 + row < sure) return;
     bool odd = false;
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) odd |= !isfinite(bf16_hi(vp[i])) || !isfinite(bf16_lo(vp[i]));
+    for (int i = 0; i < D / 64; ++i) odd |= !isfinite(bf16_hi(vp[i])) || !(fabsf(bf16_lo(vp[i])) < 0x1p125f);
     if (odd) {
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
@@ -269,7 +287,7 @@ __device__ __forceinline__ void chunk_put(bool value, const Kv4AttendParams& p, 
     const ChunkPiece c = chunk_piece(p, walk, units);
     u += units;
     if (c.most == 0) continue;
-    int size = 0;  // exponent of the unit: K's of the tile, V's so far in this piece
+    int size = 0;  // exponent of the common unit: K's of the tile, V's so far in this piece
     const int len = walk.rq.len, sure = kv4_sees(p, walk.rq, c.row0);
     locate(c, len, 0, page_of(c, len, 0));
     fetch_par(c, sure, 0);
@@ -277,9 +295,17 @@ __device__ __forceinline__ void chunk_put(bool value, const Kv4AttendParams& p, 
     int id = page_of(c, len, 1);  // of the next tile's key
     for (int j = 0; j < c.most; ++j, ++g) {
       const int s = g % S, slot = g & 3;
+      const bool own = chunk_own(c.k0 + j, len, sure);
+      int mine = 0;
+      if (!value || own) mine = size_of(value ? vp : kp);
       if (!value) {
-        const int ek = __reduce_max_sync(0xffffffffu, size_of(kp));
-        const int ev = __reduce_max_sync(0xffffffffu, size_of(vp));
+        const int v_size = size_of(vp);
+        if (own) {
+          cs.own_up[slot][0][row] = chunk_up(chunk_size(mine)) * 0x1p-32f;
+          cs.own_up[slot][1][row] = chunk_up(chunk_size(v_size)) * 0x1p-32f;
+        }
+        const int ek = __reduce_max_sync(0xffffffffu, mine);
+        const int ev = __reduce_max_sync(0xffffffffu, v_size);
         const uint32_t absent = __ballot_sync(0xffffffffu, gone);
         if (lane == 0) {
           cs.size[slot][in_group][0] = ek;
@@ -290,16 +316,15 @@ __device__ __forceinline__ void chunk_put(bool value, const Kv4AttendParams& p, 
       }
       if (!wait_bounded_warp(bar(L::kSize + slot), (g >> 2) & 1, p.limit_ns, abort_flag, err)) return;
       if (!value) size = 0;
+      if (!own) {
 #pragma unroll
-      for (int w = 0; w < 4; ++w) size = max(size, cs.size[slot][w][value ? 1 : 0]);
-      // the largest value to [2^-8, 2^-7): scale 2^24 stays below fp16's largest
-      // (exponents kept where both powers are normal numbers: values from 2^119
-      // on come out infinite)
-      const int x = min(max(size, 20), 245);
-      if (!value && row == 0) cs.k_up[slot] = __uint_as_float(static_cast<uint32_t>(x + 8) << 23);
-      const float unit = __uint_as_float(static_cast<uint32_t>(246 - x) << 23);
-      const PutFactors f0(value ? vp[0] : kp[0], unit);
-      const PutFactors f1(value ? vp[D / 64 - 1] : kp[D / 64 - 1], unit);
+        for (int w = 0; w < 4; ++w) size = max(size, cs.size[slot][w][value ? 1 : 0]);
+      }
+      const int x = chunk_size(own ? mine : size);
+      if (!value && row == 0) cs.k_up[slot] = chunk_up(x);
+      const float down = chunk_down(x);
+      const PutFactors f0(value ? vp[0] : kp[0], down);
+      const PutFactors f1(value ? vp[D / 64 - 1] : kp[D / 64 - 1], down);
       // where K's word is of the first group and V's of the second, and conversely
       const PutFactors f01 = value ? f1 : f0, f10 = value ? f0 : f1;
       locate(c, len, j + 1, id);
@@ -311,7 +336,7 @@ __device__ __forceinline__ void chunk_put(bool value, const Kv4AttendParams& p, 
         const int wk = 4 * (i % (D / 32)) + i / (D / 32), wv = 8 * (i % (D / 64)) + i / (D / 64);
         const PutFactors& f = (wk >> 3) == 0 ? ((wv >> 3) == 0 ? f0 : f01) : ((wv >> 3) == 0 ? f10 : f1);
         const uint32_t to_k = (wk >> 3) * 16384 + (wk & 7) * 16, to_v = (wv >> 3) * 16384 + (wv & 7) * 16;
-        const uint4 v = put_word(code[i], f.s24, f.s20, f.lo);
+        const uint4 v = put_word(code[i], f.s9, f.lo);
         st_shared_v4((base + s * L::kTile + (value ? to_v : to_k)) ^ turn, v.x, v.y, v.z, v.w);
       }
       fetch_codes();
@@ -320,6 +345,82 @@ __device__ __forceinline__ void chunk_put(bool value, const Kv4AttendParams& p, 
       if (lane == 0) mbar_arrive(bar(full + s));
     }
   }
+}
+
+// Multiplies a row's P of the first 32 cols columns of S.
+__device__ __forceinline__ void chunk_fall(uint32_t s_addr, int cols, float less) {
+  tmem_wait_st();
+#pragma unroll 1
+  for (int w = 0; w < cols; ++w) {
+    uint32_t old[16];
+    tmem_ld_32x32b_x16(s_addr + 16 * w, old);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      asm volatile("" : "+r"(old[i]));
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&old[i]));
+      old[i] = pack_f16x2(v.x * less, v.y * less);
+    }
+    tmem_st_32x32b_x16(s_addr + 16 * w, old);
+  }
+}
+
+// The softmax of a row over a tile of own units (`up`: the keys' units of K, then
+// of V, times 2^-32): P of a key is its probability times V's unit over the row's,
+// which moves where a product passes 2^15.  Columns from `left` on are hidden.
+// Out of line: beside the ordinary tiles' code, and hardly ever run, it cost them
+// a tenth of their speed (1000-token chunk 403 -> 449 us).
+struct OwnTile {
+  float m, v_up, alpha, beta, sum;  // alpha: for l and O; beta: for O besides
+};
+__device__ __forceinline__ OwnTile chunk_own_tile(uint32_t s_addr, const float* up, const uint32_t* absent,
+                                               float factor, int left, float m, float v_up) {
+  OwnTile r = {m, v_up, 1.f, 1.f, 0.f};
+  const float to_log2 = factor * 0x1p32f;
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q) {
+    uint32_t x[32];
+    tmem_ld_32x32b_x32(s_addr + 32 * q, x);
+    tmem_wait_ld_regs(x);
+    const int here = min(max(left - 32 * q, 0), 32);  // columns before it are seen
+    const uint32_t seen = (here == 32 ? ~0u : (1u << here) - 1u) & ~absent[q];
+    float s[32], hi = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      s[i] = (seen >> i) & 1u ? __uint_as_float(x[i]) * (up[32 * q + i] * to_log2) : -INFINITY;
+      hi = fmaxf(hi, s[i]);
+    }
+    const bool over = hi - r.m > 14.f;
+    if (__any_sync(0xffffffffu, over)) {
+      const float less = over ? ex2_approx(r.m - hi) : 1.f;
+      r.m = over ? hi : r.m;
+      r.alpha *= less;
+      r.sum *= less;
+      chunk_fall(s_addr, q, less);
+    }
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float e = ex2_approx(s[i] - r.m);
+      r.sum += e;
+      s[i] = e * up[128 + 32 * q + i];
+      top = fmaxf(top, s[i]);
+    }
+    const bool large = top * (1.f / r.v_up) > 32768.f;
+    if (__any_sync(0xffffffffu, large)) {  // the largest to [8, 16)
+      const float next = __uint_as_float((max(__float_as_uint(top) >> 23, 4u) - 3u) << 23);
+      const float less = large ? r.v_up / next : 1.f;
+      r.v_up = large ? next : r.v_up;
+      r.beta *= less;
+      chunk_fall(s_addr, q, less);
+    }
+    const float down = 1.f / r.v_up;
+    uint32_t pk[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) pk[i] = pack_f16x2(s[2 * i] * down, s[2 * i + 1] * down);
+    tmem_st_32x32b_x16(s_addr + 16 * q, pk);
+  }
+  return r;
 }
 
 template <int D>
@@ -529,21 +630,38 @@ __global__ void __launch_bounds__(kChunkWarps * 32, 1)
         const int lim = real ? kv4_sees(p, rq, row) : 0;
         // keys that every row of this warp sees (rows past the end do not count)
         const int all_see = __reduce_min_sync(0xffffffffu, real ? lim : 0x7fffffff);
-        float m = -3.402823466e38f, l = 0.f, v_up = 0.f;
-        int v_size = 0;  // V's unit, as the V warps find it
+        const int sure = kv4_sees(p, rq, c.row0);
+        float m = -3.402823466e38f, l = 0.f;
+        float v_up = 0.f;  // the unit of O times 2^-32, 0: none yet
+        int v_size = 0;    // V's common unit, as the V warps find it
         for (int j = 0; j < n; ++j) {
           const int slot = (g + j) & 3;
           if (!(ok = wait_bounded_warp(bar(L::kSFull + t), steps & 1, limit, abort_flag, err))) break;
           ++steps;
           tc_fence_after();
-          // (not 0: a hidden key's score is minus infinity times it; scores in these
-          // units stay below 2^20)
-          const float f = fmaxf(factor * cs.k_up[slot], 1e-30f);
+          const int key0 = (c.k0 + j) * 128;
+          float alpha = 1.f;  // what l and O are to be multiplied by
+          float beta = 1.f;   // and O besides, for its unit
+          if (__builtin_expect(chunk_own(c.k0 + j, rq.len, sure), 0)) {
+            const OwnTile own = chunk_own_tile(s_addr, cs.own_up[slot][0], cs.absent[slot], factor,
+                                               lim - key0, m, v_up == 0.f ? 0x1p-126f : v_up);
+            m = own.m;
+            v_up = own.v_up;
+            alpha = own.alpha;
+            beta = own.beta;
+            l = fmaf(l, alpha, own.sum);
+          } else {
 #pragma unroll
           for (int w = 0; w < 4; ++w) v_size = max(v_size, cs.size[slot][w][1]);
-          const float next_up = __uint_as_float(static_cast<uint32_t>(min(max(v_size, 20), 245) + 8) << 23);
+          const float next_up = chunk_up(chunk_size(v_size)) * 0x1p-32f;
+          if (next_up != v_up) {
+            beta = v_up / next_up;
+            v_up = next_up;
+          }
+          // (not 0: a hidden key's score is minus infinity times it; scores in these
+          // units stay below 2^31)
+          const float f = fmaxf(factor * cs.k_up[slot], 1e-30f);
           const uint4 absent = *reinterpret_cast<const uint4*>(cs.absent[slot]);
-          const int key0 = (c.k0 + j) * 128;
           const bool masked = key0 + 128 > all_see || (absent.x | absent.y | absent.z | absent.w) != 0;
           // 32 columns at a time (one copy of this code: unrolled with the next
           // columns loading meanwhile it is 3 % slower, for the instruction cache):
@@ -551,7 +669,6 @@ __global__ void __launch_bounds__(kChunkWarps * 32, 1)
           // alongside; where some row's passes its reference by 2^14 the reference
           // moves, the columns are done again, and the probabilities of this tile
           // already written, the sums, and below O follow
-          float alpha = 1.f;  // what O is to be multiplied by
           float2 sum = make_float2(0.f, 0.f);
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
@@ -593,29 +710,14 @@ __global__ void __launch_bounds__(kChunkWarps * 32, 1)
               alpha *= less;
               before.x *= less;
               before.y *= less;
-              tmem_wait_st();
-#pragma unroll 1
-              for (int w = 0; w < q; ++w) {
-                uint32_t old[16];
-                tmem_ld_32x32b_x16(s_addr + 16 * w, old);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  asm volatile("" : "+r"(old[i]));
-                  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&old[i]));
-                  old[i] = pack_f16x2(v.x * less, v.y * less);
-                }
-                tmem_st_32x32b_x16(s_addr + 16 * w, old);
-              }
+              chunk_fall(s_addr, q, less);
             }
             tmem_st_32x32b_x16(s_addr + 16 * q, pk);
           }
           l = fmaf(l, alpha, sum.x + sum.y);
-          // ---- O follows the reference and V's unit
-          if (next_up != v_up) {
-            alpha *= v_up / next_up;
-            v_up = next_up;
           }
+          // ---- O follows the reference and its unit
+          alpha *= beta;
           if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
             // (S of this tile was issued after the last P V, which is done)
 #pragma unroll 1
@@ -641,7 +743,8 @@ __global__ void __launch_bounds__(kChunkWarps * 32, 1)
           ++finals;
           tc_fence_after();
         }
-        const float scale_o = n == 0 || l == 0.f ? 0.f : c.whole ? v_up / l : v_up;
+        const float unit_o = v_up * 0x1p32f;
+        const float scale_o = n == 0 || l == 0.f ? 0.f : c.whole ? unit_o / l : unit_o;
         const float m_out = m == -3.402823466e38f && l == 0.f ? -INFINITY : m;
 #pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {

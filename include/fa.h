@@ -344,8 +344,13 @@ FA_API fa_status fa_kv4_gather(const void* cache, const long long* slots, void* 
  * Deterministic: the same arguments give the same bits.
  * Precision: up to 47 rows a kv head (max_tokens * heads / kv_heads; 79 at
  * d = 64) the scores are those of the cached values to 32 bits; above, keys and
- * values go through fp16 (2^-12 of themselves on average).  P is fp16, O and
- * the statistics 32 bits, O is rounded once.
+ * values go through fp16: each is off by at most 2^-11 of itself and 2^-11 of its
+ * group's lowest, or 2^-33 of the largest key of its 128 tokens, the largest value
+ * of the row's tokens so far, if that is more.  P is fp16 in a unit that follows
+ * the row, below its normal numbers 2^-25 of it; O and the statistics are 32 bits
+ * (the sums of P V before the division included: values from about 2^110 on can
+ * overflow them), O is rounded once.
+ * What tokens hold that a row does not see changes none of its bits.
  * A cached key or value that is no number (see fa_kv4_append) makes the rows
  * that see it NaN, in its 64 channels or in all, and no other row.
  *   workspace : fa_kv4_attention_workspace_size bytes, 16-byte aligned,

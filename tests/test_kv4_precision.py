@@ -19,6 +19,14 @@ MMA = [
     (128, 8, 1, 16, [260], [5]),
     (64, 4, 1, 64, [1100], [19]),
 ]
+TCGEN = [
+    (128, 8, 2, 16, [150], [50]),
+    (64, 16, 2, 32, [700], [60]),
+    (128, 4, 4, 64, [600], [300]),
+    (64, 1, 1, 16, [400], [400]),
+]
+
+
 def on_tcgen(c):
     rows = c.most * (c.q.shape[1] // c.cache.shape[1])
     return rows >= (80 if c.d == 64 else 48)
@@ -58,7 +66,7 @@ def attend(c, causal=True, scale=None):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("shape", MMA, ids=lambda s: "-".join(map(str, s)).replace(" ", ""))
+@pytest.mark.parametrize("shape", MMA + TCGEN, ids=lambda s: "-".join(map(str, s)).replace(" ", ""))
 @pytest.mark.parametrize("value", [False, True], ids=["key", "value"])
 def test_rows_do_not_depend_on_tokens_they_do_not_see(shape, value):
     """One of a request's new tokens grows by powers of two up to the largest floats,
@@ -99,7 +107,8 @@ def check(c, o, lse, causal=True, scale=None):
         2^-8 of the largest |v| seen;
       * V, tcgen05: 2^-11 of |lowest| and of |v|, and 2^-33 of the largest seen (in
         units that bring that one to 2^8 at least), twice;
-      * O: its rounding, and 2^-20 of its terms for fp32 sums.
+      * O: its rounding (2^-25 where fp16 holds it as a subnormal number, below
+        2^-14), and 2^-20 of its terms for fp32 sums.
     """
     d, tc = c.d, on_tcgen(c)
     scale = d ** -0.5 if scale is None else scale
@@ -139,7 +148,8 @@ def check(c, o, lse, causal=True, scale=None):
             tl = -torch.log1p(-(p * torch.expm1(eta)).sum(1)) + 2.0 ** -20 + 2.0 ** -22 * ll.abs()
             oo = p @ v
             spans = v8 * 15 / 8
-            to = u * oo.abs() + pe @ v.abs() + pe.sum(1, keepdim=True) * oo.abs() + 2.0 ** -20 * (p @ (v.abs() + spans))
+            tiny = 2.0 ** -25 if c.q.dtype == torch.float16 else 0.0
+            to = (u * oo.abs()).clamp_min(tiny) + pe @ v.abs() + pe.sum(1, keepdim=True) * oo.abs() + 2.0 ** -20 * (p @ (v.abs() + spans))
             most = p.amax(1, keepdim=True)
             if tc:
                 low = vlo.abs().repeat_interleave(64, 1)
@@ -160,7 +170,7 @@ def check(c, o, lse, causal=True, scale=None):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("heads", [4], ids=["mma"])
+@pytest.mark.parametrize("heads", [4, 64], ids=["mma", "tcgen05"])
 @pytest.mark.parametrize("ratio", [0, 10, 16])
 @pytest.mark.parametrize("keys", [1, 40])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
@@ -179,8 +189,9 @@ def test_groups_of_unlike_sizes_keep_their_bits(heads, ratio, keys, dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("shape", [(128, 4, 1, 16, [1000, 90], [1, 3]), (64, 8, 2, 16, [600], [4]),
-                                   (128, 16, 2, 32, [700], [5])],
-                         ids=["mma128", "mma64", "mma128x5"])
+                                   (128, 16, 2, 32, [700], [5]), (128, 16, 2, 16, [1000, 200], [8, 60]),
+                                   (64, 32, 2, 64, [900], [40])],
+                         ids=["mma128", "mma64", "mma128x5", "tcgen128", "tcgen64"])
 @pytest.mark.parametrize("power", [8, 12, 16, 20])
 def test_a_large_token_of_no_weight_takes_no_bits(shape, power):
     """A token that all rows see has values 2^power larger than all others and a
@@ -196,7 +207,7 @@ def test_a_large_token_of_no_weight_takes_no_bits(shape, power):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("heads", [4], ids=["mma"])
+@pytest.mark.parametrize("heads", [4, 64], ids=["mma", "tcgen05"])
 def test_a_large_key_takes_no_bits_from_its_tile(heads):
     """Every eighth token's keys are 2^12 larger and opposed to the queries (no weight):
     the others' scores keep their precision."""
@@ -209,7 +220,7 @@ def test_a_large_key_takes_no_bits_from_its_tile(heads):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("heads", [4], ids=["mma"])
+@pytest.mark.parametrize("heads", [4, 64], ids=["mma", "tcgen05"])
 def test_values_and_keys_near_the_ends_of_the_floats(heads):
     """One key: O is its value and LSE its score, from 2^-90 to 2^120."""
     for power in (-90, -40, 60, 100, 120):
