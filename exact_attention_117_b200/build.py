@@ -3,8 +3,8 @@
     python -m exact_attention_117_b200.build [--debug]  (or __graft_entry__.build())
 
 ``--debug`` builds ``libfa_b200_debug.so`` with ``-DFA_DEBUG``: the same
-kernels with every TMA coordinate, TMEM column range and directly indexed
-global address checked before use (a failed check is reported through the
+kernels with the TMA coordinates, TMEM column ranges and directly indexed
+global addresses checked before use (a failed check is reported through the
 device error word, see ``fa_check_device_error``).  Point the binding at it
 with the ``FA_LIBRARY`` environment variable.  The release build also compiles
 ``_fa_binding.so`` (csrc/binding.cpp, host code) with g++ against torch.

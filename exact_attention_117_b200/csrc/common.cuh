@@ -28,16 +28,20 @@ enum : unsigned int {
   kErrAlign = 1u << 14,      // dynamic shared memory base not 1 KiB aligned
   kErrSelfTest = 1u << 15,   // the watchdog self-test kernel gave up (as it must)
   kErrBadPage = 1u << 16,    // a page index of a block table lies outside the cache
-  kErrKv4 = 1u << 4,         // attention over the 4-bit cache
+  kErrKv4 = 1u << 4,         // the 4-bit cache: plan, append, gather, attention
+  kErrRotary = 1u << 5,      // rotary positions
   kErrDebugCheck = 1u << 17, // a bounds check of the FA_DEBUG build failed (see dbg_check)
 };
 
 // ---------------------------------------------------------- debug build
-// Built with -DFA_DEBUG, the kernels check every TMA coordinate, shared-memory
-// destination, TMEM column range and directly indexed global address before
-// using it.  A failed check records kErrDebugCheck and the role's code in the
-// error word, raises the CTA's abort flag and skips the access, so the CTA
-// leaves through the same path as a timed-out wait (no trap, no assert).
+// Built with -DFA_DEBUG, the kernels check TMA coordinates, shared-memory
+// destinations, TMEM column ranges and directly indexed global addresses before
+// using them: of the training kernels each, of the serving kernels those that
+// follow from lengths, slots, tables and the split of the work (cache tiles, table
+// and ring places, packed rows, partial results).  A failed check records
+// kErrDebugCheck and the role's code in the error word and skips the access; a
+// kernel with roles raises the CTA's abort flag and leaves through the same path
+// as a timed-out wait (no trap, no assert).
 #ifdef FA_DEBUG
 constexpr bool kDebugChecks = true;
 #else
@@ -48,6 +52,14 @@ __device__ __forceinline__ bool dbg_check(bool cond, unsigned int code, volatile
   if (!kDebugChecks || cond) return true;
   atomicOr(&g_error_word, kErrDebugCheck | code);
   *abort_flag = 1;
+  return false;
+}
+
+// The same for a kernel without roles that could leave early: the caller skips
+// the one access.
+__device__ __forceinline__ bool dbg_access(bool cond, unsigned int code) {
+  if (!kDebugChecks || cond) return true;
+  atomicOr(&g_error_word, kErrDebugCheck | code);
   return false;
 }
 

@@ -100,6 +100,14 @@ __device__ __forceinline__ int store_places(const Kv4StoreParams& p, long long t
   __syncthreads();
   return n;
 }
+// The cache's bytes; all that a thread of append or gather touches of row `row`
+// at `first` lies inside.
+template <int D>
+__device__ __forceinline__ bool store_inside(const Kv4StoreParams& p, long long first, int next, int par) {
+  const long long bytes = (p.n_slots >> 4) * p.heads * Kv4Tile<D>::kBytes;
+  return dbg_access(first >= 0 && first + next + 4 <= bytes && first + par >= 0 && first + par + 4 <= bytes,
+                    kErrKv4);
+}
 
 // The pair of words a thread keeps: where it lies in x and in a tile.
 template <int D>
@@ -228,7 +236,9 @@ __device__ __forceinline__ void append_words(const Kv4StoreParams& p, const Stor
                   : __byte_perm(__float_as_uint(four[2 * i] + 0x1p23f),
                                 __float_as_uint(four[2 * i + 1] + 0x1p23f), 0x5410);
   if (tile < 0) return;
-  uint8_t* at = p.cache + tile + w.in_cache + row * L::kRow;
+  const long long first = tile + w.in_cache + row * L::kRow;
+  if (!store_inside<D>(p, first, w.next, w.par(row))) return;
+  uint8_t* at = p.cache + first;
   *reinterpret_cast<uint32_t*>(at) = code[0];
   *reinterpret_cast<uint32_t*>(at + w.next) = code[1];
   if ((w.word & 7) == 0) *reinterpret_cast<uint32_t*>(at + w.par(row)) = par;
@@ -293,7 +303,9 @@ __global__ void __launch_bounds__(kStoreThreads) kv4_gather_kernel(const __grid_
       for (int u = 0; u < kStoreBatch; ++u) {
         const int tk = t + u * p.side_by_side;
         if (tk >= n || sp.tile[tk] < 0) continue;
-        const uint8_t* at = p.cache + sp.tile[tk] + w.in_cache + sp.row[tk] * L::kRow;
+        const long long first = sp.tile[tk] + w.in_cache + sp.row[tk] * L::kRow;
+        if (!store_inside<D>(p, first, w.next, w.par(sp.row[tk]))) continue;
+        const uint8_t* at = p.cache + first;
         code[u][0] = __ldg(reinterpret_cast<const uint32_t*>(at));
         code[u][1] = __ldg(reinterpret_cast<const uint32_t*>(at + w.next));
         par[u] = __ldg(reinterpret_cast<const uint32_t*>(at + w.par(sp.row[tk])));
@@ -516,6 +528,11 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const __grid_con
         pos[u] = s_old[i[u]] + (t0 + u * step - s_cu[i[u]]);
         const int n = static_cast<int>(p.by_page(pos[u])), held = s_held[i[u]];
         in_page[u] = pos[u] - n * p.page_size;
+        page[u] = 0;
+        if (!dbg_access(n >= 0 && n < p.width && t0 + u * step < p.max_tokens &&
+                            (n < held || (n - held >= 0 && s_need[i[u]] + n - held < p.ring_size)),
+                        kErrKv4))
+          continue;
         page[u] = n < held ? p.table[(b0 + i[u]) * p.table_stride + n]
                            : *ring_at(s_head, s_need[i[u]] + n - held);
       }
@@ -528,11 +545,15 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const __grid_con
     }
     for (int k = base_need + me; k < need_end; k += step) {
       const int i = plan_find(s_need, cnt, k);
+      if (!dbg_access(k < p.ring_size && s_held[i] + (k - s_need[i]) < p.width, kErrKv4)) continue;
       p.table[(b0 + i) * p.table_stride + s_held[i] + (k - s_need[i])] = *ring_at(s_head, k);
     }
     for (int k = base_back + me; k < back_end; k += step) {
       const int i = plan_find(s_back, cnt, k);
       const int rows = s_back[i + 1] - s_back[i];
+      if (!dbg_access(k < p.ring_size && s_held[i] - rows >= 0 && s_held[i] - rows + (k - s_back[i]) < p.width,
+                      kErrKv4))
+        continue;
       *ring_at(s_tail, k) = p.table[(b0 + i) * p.table_stride + s_held[i] - rows + (k - s_back[i])];
     }
     base_cu = cu_end;

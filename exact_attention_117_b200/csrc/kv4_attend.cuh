@@ -49,6 +49,7 @@ struct Kv4AttendParams {
   const int* lengths;
   const int* cu_tokens;
   float* part;            // partial results: 2 per CTA
+  long long part_floats;  // room for them
   struct Kv4Cut* cuts;    // of kv4_chunk.cuh: one per CTA
   long long q_st, q_sh, o_st, o_sh;  // strides in elements
   long long table_stride;
@@ -318,6 +319,7 @@ __device__ __forceinline__ void kv4_store_row(const Kv4AttendParams& p, const Kv
                                               int row, int lane, const float (&o)[D / 32], float m,
                                               float l) {
   const int i = p.by_group(row), tok = rq.first + i, head = h * p.group + row - i * p.group;
+  if (!dbg_access(row >= 0 && row < rq.rows && tok < p.tokens && head < p.heads, kErrKv4)) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const long long at = tok * p.o_st + head * p.o_sh + lane * (D / 32);
   uint32_t w[D / 64];
@@ -351,7 +353,7 @@ __device__ __forceinline__ void kv4_rows(const Kv4AttendParams& p, const Kv4Req&
 #pragma unroll
   for (int j = 0; j < D / 32; ++j) {
     uint4 raw = make_uint4(0, 0, 0, 0);
-    if (r < rows)
+    if (r < rows && dbg_access(rq.first + i < p.tokens && h < p.kv_heads && row0 + r < rq.rows, kErrKv4))
       raw = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at + 32 * j + 8 * t);
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
@@ -720,7 +722,12 @@ __global__ void __launch_bounds__(kKv4Warps * 32, (Kv4AttendLayout<D, NT>::kCtas
     auto look_up = [&]() {
       from = -1;
       if (lane < kBT && tile < tile_end) {
-        const int page = p.page_tiles(tile), id = table[page];
+        const int page = p.page_tiles(tile);
+        const int id = dbg_access(tile >= 0 && page < p.width && tile - page * tiles_per_page < tiles_per_page &&
+                                      b < p.requests && h < p.kv_heads,
+                                  kErrKv4)
+                           ? table[page]
+                           : -1;
         if (static_cast<unsigned>(id) < static_cast<unsigned>(p.pages))
           from = id * page_bytes + static_cast<long long>(tile - page * tiles_per_page) * T::kBytes;
         else
@@ -886,7 +893,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, (Kv4AttendLayout<D, NT>::kCtas
       }
       if (whole)
         kv4_store_row<D>(p, rq, h, row0 + r, lane, o, top, sum);
-      else {
+      else if (dbg_access(part + L::kPartFloats <= p.part + p.part_floats, kErrKv4)) {
         store_floats<D / 32>(part + r * D + lane * (D / 32), o);
         if (lane == 0) {
           part[L::kRows * D + r] = top;
@@ -936,6 +943,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32)
     return p.part + (2LL * (first + k) + (k == 0 && share.start(first) <= u0 ? 1 : 0)) * L::kPartFloats;
   };
   const int n = last - first + 1;
+  if (!dbg_access(first >= 0 && last < ctas && 2LL * ctas * L::kPartFloats <= p.part_floats, kErrKv4)) return;
   float top = -INFINITY;
   for (int k = lane; k < n; k += 32) top = fmaxf(top, piece(k)[L::kRows * D + r]);
 #pragma unroll

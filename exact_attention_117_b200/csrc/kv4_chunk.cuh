@@ -222,7 +222,11 @@ __device__ __forceinline__ void chunk_put(bool value, const Kv4AttendParams& p, 
   bool gone = false;            // its page lies outside the cache
   auto page_of = [&](const ChunkPiece& c, int len, int j) {
     const int key = (c.k0 + j) * 128 + row;
-    return j < c.most && key < len ? p.table[c.b * p.table_stride + p.page_tiles(key >> 4)] : -1;
+    return j < c.most && key < len &&
+                   dbg_check(key >= 0 && static_cast<int>(p.page_tiles(key >> 4)) < p.width && c.b < p.requests,
+                             err, abort_flag)
+               ? p.table[c.b * p.table_stride + p.page_tiles(key >> 4)]
+               : -1;
   };
   auto locate = [&](const ChunkPiece& c, int len, int j, int id) {
     const int key = (c.k0 + j) * 128 + row, tile = key >> 4;
@@ -231,6 +235,10 @@ __device__ __forceinline__ void chunk_put(bool value, const Kv4AttendParams& p, 
     gone = live && !in;
     if (!value && gone) atomicOr(&g_error_word, kErrBadPage);
     const int place = tile - static_cast<int>(p.page_tiles(tile)) * tiles_per_page;
+    if (!dbg_check(!in || (place >= 0 && place < tiles_per_page && c.h < p.kv_heads), err, abort_flag)) {
+      at = nullptr;
+      return;
+    }
     at = in ? p.cache + ((static_cast<long long>(id) * p.kv_heads + c.h) * tiles_per_page + place) * T::kBytes
             : nullptr;
   };
@@ -581,6 +589,12 @@ __global__ void __launch_bounds__(kChunkWarps * 32, 1)
         const bool real = in_tile < c.rows;
         const int tok = p.by_group(row), head = c.h * p.group + row - tok * p.group;
         const int n = c.tiles[t];
+        if (!(ok = __all_sync(0xffffffffu, dbg_check(tmem_range_ok(s_addr, tmem, 128, L::kTmemCols) &&
+                                                         tmem_range_ok(o_addr, tmem, D, L::kTmemCols) &&
+                                                         (!real || (rq.first + tok < p.tokens && head < p.heads)) &&
+                                                         part + L::kPartFloats <= p.part + p.part_floats,
+                                                     err, abort_flag))))
+          break;
         float factor = 0.f;  // from scores in the tile's units to base-2 exponents
         if (n > 0) {
           // ---- this row of Q: fp16 times a power of two, in the channel order
@@ -815,6 +829,10 @@ __global__ void __launch_bounds__(kChunkJoinWarps * 32)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Kv4Cut cut = p.cuts[blockIdx.x + 1];
   if (r >= cut.rows) return;
+  if (!dbg_access(cut.first >= 0 && cut.first + cut.pieces <= ctas && cut.rows <= kChunkRows &&
+                      2LL * ctas * L::kPartFloats <= p.part_floats,
+                  kErrKv4))
+    return;
   auto piece = [&](int k) {
     return p.part + (2LL * (cut.first + k) + (k == 0 ? cut.second : 0)) * L::kPartFloats;
   };
@@ -827,6 +845,7 @@ __global__ void __launch_bounds__(kChunkJoinWarps * 32)
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int row = cut.row0 + r, i = p.by_group(row), head = cut.h * p.group + row - i * p.group;
   const long long tok = cut.token0 + i;
+  if (!dbg_access(tok < p.tokens && head < p.heads, kErrKv4)) return;
   uint16_t* to = static_cast<uint16_t*>(p.o) + tok * p.o_st + head * p.o_sh;
   constexpr int kEach = D / 4 / kChunkJoinWarps;  // groups of four channels of a warp
   float4 o[kEach] = {};

@@ -410,6 +410,7 @@ fa_status fa_kv4_attention(const void* q, const void* cache, const int* block_ta
   p.lengths = lengths;
   p.cu_tokens = cu_tokens;
   p.part = static_cast<float*>(workspace);
+  p.part_floats = static_cast<long long>(ws.cuts_at / sizeof(float));
   p.cuts = reinterpret_cast<fa::Kv4Cut*>(static_cast<char*>(workspace) + ws.cuts_at);
   p.q_st = strides[0];
   p.q_sh = strides[1];

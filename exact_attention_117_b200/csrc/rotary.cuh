@@ -27,7 +27,7 @@
 #include <cstdint>
 #include <type_traits>
 
-#include "sm100.cuh"
+#include "common.cuh"
 
 namespace fa {
 
@@ -140,7 +140,11 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
   // The thread's heads: every head_lanes-th of the block's range, which is cut
   // into the queries' heads and the keys'.
   const int first = group * p.block_heads;
-  const int end = live ? min(first + p.block_heads, p.heads[0] + p.heads[1]) : 0;
+  int end = live ? min(first + p.block_heads, p.heads[0] + p.heads[1]) : 0;
+  if (!dbg_access(!live || (n >= 0 && e >= 0 && e + V <= (turned ? (kInterleaved ? p.rot : p.rot / 2) : p.d) &&
+                            (pos + 1) * pairs <= kRotaryPairs && first >= 0),
+                  kErrRotary))
+    end = 0;
   const T* x[2];
   T* y[2];
   int count[2];
