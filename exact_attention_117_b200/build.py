@@ -6,8 +6,9 @@
 kernels with the TMA coordinates, TMEM column ranges and directly indexed
 global addresses checked before use (a failed check is reported through the
 device error word, see ``fa_check_device_error``).  Point the binding at it
-with the ``FA_LIBRARY`` environment variable.  The release build also compiles
-``_fa_binding.so`` (csrc/binding.cpp, host code) with g++ against torch.
+with the ``FA_LIBRARY`` environment variable.  Both also compile
+``_fa_binding.so`` (csrc/binding.cpp, host code) with g++ against torch, again when
+torch or Python is another one.
 """
 from __future__ import annotations
 
@@ -52,11 +53,26 @@ def _stale(lib: str) -> bool:
     return any(os.path.getmtime(p) > t for p in deps if os.path.exists(p))
 
 
+def binding_target() -> str:
+    """What the extension module is built for, kept beside it in ``_fa_binding.so.for``:
+    its code depends on torch's and Python's binary interfaces."""
+    import torch
+    return f"torch {torch.__version__} {sys.implementation.cache_tag}\n"
+
+
+def binding_built_for() -> str:
+    try:
+        with open(BINDING + ".for") as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
 def _build_binding(force: bool, verbose: bool):
     """csrc/binding.cpp: the Python module between torch tensors and the C ABI."""
     src = os.path.join(CSRC, "binding.cpp")
     deps = [src, os.path.join(ROOT, "include", "fa.h")]
-    if not force and os.path.exists(BINDING) and \
+    if not force and os.path.exists(BINDING) and binding_built_for() == binding_target() and \
             all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
         return
     import torch
@@ -74,12 +90,13 @@ def _build_binding(force: bool, verbose: bool):
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
     os.replace(tmp, BINDING)
+    with open(BINDING + ".for", "w") as f:
+        f.write(binding_target())
 
 
 def build(force: bool = False, verbose: bool = False, extra=(), debug: bool = False) -> str:
     lib = DEBUG_LIB if debug else LIB
-    if not debug:
-        _build_binding(force, verbose)
+    _build_binding(force and not debug, verbose)
     if not force and not _stale(lib):
         return lib
     tmp = lib + ".tmp"

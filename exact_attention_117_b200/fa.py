@@ -111,6 +111,10 @@ def _load_native():
         if not os.path.exists(path):
             raise RuntimeError(f"binding not built: {path} is missing "
                                "(run __graft_entry__.build())")
+        from . import build
+        if build.binding_built_for() not in ("", build.binding_target()):  # ("": not said)
+            raise RuntimeError(f"{path} was built for another torch or Python "
+                               "(run __graft_entry__.build())")
         spec = importlib.util.spec_from_file_location("_fa_binding", path)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
