@@ -131,6 +131,10 @@ def check(c, o, lse, causal=True, scale=None):
             if causal:
                 see = (n - new + 1 + torch.arange(new, device="cuda")).clamp(0, n)
             see = see.repeat_interleave(H // G)
+            got_o = o[first:last, heads].double().reshape(-1, d)
+            got_l = lse[first:last, heads].double().reshape(-1)
+            assert not got_o[see == 0].any() and (got_l[see == 0] == -math.inf).all()
+            q, got_o, got_l, see = q[see > 0], got_o[see > 0], got_l[see > 0], see[see > 0]
             hidden = torch.arange(n, device="cuda") >= see[:, None]
             seen = (~hidden).double()
             s = (q @ k.T * scale).masked_fill(hidden, -math.inf)
@@ -161,8 +165,6 @@ def check(c, o, lse, causal=True, scale=None):
                 step = groups(spans)[..., 0]  # 15 scales of each key and group
                 big = (p[:, :, None] * step[None]).amax(1).repeat_interleave(64, 1)
                 to = to + 2.0 ** -11 * (p @ spans) + n * 2.0 ** -28 * big
-            got_o = o[first:last, heads].double().reshape(-1, d)
-            got_l = lse[first:last, heads].double().reshape(-1)
             over = ((got_o - oo).abs() / to.clamp_min(1e-300)).amax()
             assert ((got_o - oo).abs() <= to).all(), f"O off by {float(over):.2f} of the bound"
             over = ((got_l - ll).abs() / tl).amax()
