@@ -376,15 +376,15 @@ __device__ __forceinline__ void chunk_fall(uint32_t s_addr, int cols, float less
 // The softmax of a row over a tile of own units (`up`: the keys' units of K, then
 // of V, times 2^-32): P of a key is its probability times V's unit over the row's,
 // which moves where a product passes 2^15.  Columns from `left` on are hidden.
-// Out of line: beside the ordinary tiles' code, and hardly ever run, it cost them
-// a tenth of their speed (1000-token chunk 403 -> 449 us).
+// Out of line, for tiles after the ordinary ones: as a part of their loop it cost
+// that a tenth of its speed (1000-token chunk 403 -> 449 us).
 struct OwnTile {
-  float m, v_up, alpha, beta, sum;  // alpha: for l and O; beta: for O besides
+  float m, v_up, alpha, sum;  // alpha: for l and O
 };
-__device__ __forceinline__ OwnTile chunk_own_tile(uint32_t s_addr, const float* up, const uint32_t* absent,
-                                               float factor, int left, float m, float v_up) {
-  OwnTile r = {m, v_up, 1.f, 1.f, 0.f};
-  const float to_log2 = factor * 0x1p32f;
+__device__ __noinline__ OwnTile chunk_own_tile(uint32_t s_addr, const float* up, const uint32_t* absent,
+                                                  float factor, int left, float m, float v_up) {
+  OwnTile r = {m, v_up, 1.f, 0.f};
+  const float2 to_log2 = make_float2(factor * 0x1p32f, factor * 0x1p32f);
 #pragma unroll 1
   for (int q = 0; q < 4; ++q) {
     uint32_t x[32];
@@ -392,11 +392,15 @@ __device__ __forceinline__ OwnTile chunk_own_tile(uint32_t s_addr, const float* 
     tmem_wait_ld_regs(x);
     const int here = min(max(left - 32 * q, 0), 32);  // columns before it are seen
     const uint32_t seen = (here == 32 ? ~0u : (1u << here) - 1u) & ~absent[q];
-    float s[32], hi = -INFINITY;
+    float hi = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      s[i] = (seen >> i) & 1u ? __uint_as_float(x[i]) * (up[32 * q + i] * to_log2) : -INFINITY;
-      hi = fmaxf(hi, s[i]);
+    for (int i = 0; i < 32; i += 2) {
+      const float2 u = *reinterpret_cast<const float2*>(up + 32 * q + i);
+      const float2 v = mul_f32x2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
+                                 mul_f32x2(u, to_log2));
+      x[i] = (seen >> i) & 1u ? __float_as_uint(v.x) : 0xff800000u;
+      x[i + 1] = (seen >> (i + 1)) & 1u ? __float_as_uint(v.y) : 0xff800000u;
+      hi = fmax3(__uint_as_float(x[i]), __uint_as_float(x[i + 1]), hi);
     }
     const bool over = hi - r.m > 14.f;
     if (__any_sync(0xffffffffu, over)) {
@@ -407,25 +411,34 @@ __device__ __forceinline__ OwnTile chunk_own_tile(uint32_t s_addr, const float* 
       chunk_fall(s_addr, q, less);
     }
     float top = 0.f;
+    float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float e = ex2_approx(s[i] - r.m);
-      r.sum += e;
-      s[i] = e * up[128 + 32 * q + i];
-      top = fmaxf(top, s[i]);
+    for (int i = 0; i < 32; i += 2) {
+      const float2 u = *reinterpret_cast<const float2*>(up + 128 + 32 * q + i);
+      const float2 y = add_f32x2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
+                                 make_float2(-r.m, -r.m));
+      const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+      sum = add_f32x2(sum, e);
+      const float2 v = mul_f32x2(e, u);
+      top = fmax3(v.x, v.y, top);
+      x[i] = __float_as_uint(v.x);
+      x[i + 1] = __float_as_uint(v.y);
     }
-    const bool large = top * (1.f / r.v_up) > 32768.f;
+    r.sum += sum.x + sum.y;
+    const bool large = top > 32768.f * r.v_up;
     if (__any_sync(0xffffffffu, large)) {  // the largest to [8, 16)
       const float next = __uint_as_float((max(__float_as_uint(top) >> 23, 4u) - 3u) << 23);
       const float less = large ? r.v_up / next : 1.f;
       r.v_up = large ? next : r.v_up;
-      r.beta *= less;
       chunk_fall(s_addr, q, less);
     }
-    const float down = 1.f / r.v_up;
+    const float2 down = make_float2(1.f / r.v_up, 1.f / r.v_up);
     uint32_t pk[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) pk[i] = pack_f16x2(s[2 * i] * down, s[2 * i + 1] * down);
+    for (int i = 0; i < 16; ++i) {
+      const float2 v = mul_f32x2(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), down);
+      pk[i] = pack_f16x2(v.x, v.y);
+    }
     tmem_st_32x32b_x16(s_addr + 16 * q, pk);
   }
   return r;
@@ -589,12 +602,14 @@ __global__ void __launch_bounds__(kChunkWarps * 32, 1)
         const bool real = in_tile < c.rows;
         const int tok = p.by_group(row), head = c.h * p.group + row - tok * p.group;
         const int n = c.tiles[t];
-        if (!(ok = __all_sync(0xffffffffu, dbg_check(tmem_range_ok(s_addr, tmem, 128, L::kTmemCols) &&
-                                                         tmem_range_ok(o_addr, tmem, D, L::kTmemCols) &&
-                                                         (!real || (rq.first + tok < p.tokens && head < p.heads)) &&
-                                                         part + L::kPartFloats <= p.part + p.part_floats,
-                                                     err, abort_flag))))
-          break;
+        if (kDebugChecks) {
+          ok = __all_sync(0xffffffffu, dbg_check(tmem_range_ok(s_addr, tmem, 128, L::kTmemCols) &&
+                                                     tmem_range_ok(o_addr, tmem, D, L::kTmemCols) &&
+                                                     (!real || (rq.first + tok < p.tokens && head < p.heads)) &&
+                                                     part + L::kPartFloats <= p.part + p.part_floats,
+                                                 err, abort_flag));
+          if (!ok) break;
+        }
         float factor = 0.f;  // from scores in the tile's units to base-2 exponents
         if (n > 0) {
           // ---- this row of Q: fp16 times a power of two, in the channel order
@@ -648,30 +663,45 @@ __global__ void __launch_bounds__(kChunkWarps * 32, 1)
         float m = -3.402823466e38f, l = 0.f;
         float v_up = 0.f;  // the unit of O times 2^-32, 0: none yet
         int v_size = 0;    // V's common unit, as the V warps find it
-        for (int j = 0; j < n; ++j) {
-          const int slot = (g + j) & 3;
-          if (!(ok = wait_bounded_warp(bar(L::kSFull + t), steps & 1, limit, abort_flag, err))) break;
+        auto begin = [&]() {  // the next tile's scores
+          ok = wait_bounded_warp(bar(L::kSFull + t), steps & 1, limit, abort_flag, err);
           ++steps;
           tc_fence_after();
+          return ok;
+        };
+        // P is written: O follows the reference (alpha) and its unit
+        auto end = [&](int j, float alpha, float next_up) {
+          if (next_up != v_up) {
+            alpha *= v_up / next_up;
+            v_up = next_up;
+          }
+          if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            // (S of this tile was issued after the last P V, which is done)
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t oc[32];
+              tmem_ld_32x32b_x32(o_addr + 32 * q, oc);
+              tmem_wait_ld_regs(oc);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) oc[i] = __float_as_uint(__uint_as_float(oc[i]) * alpha);
+              tmem_st_32x32b_x32(o_addr + 32 * q, oc);
+            }
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::kPFull + t));
+        };
+        // tiles of own units are the last ones (see chunk_own)
+        const int first_own = sure >= rq.len ? n : min(max(sure / 128 - c.k0, 0), n);
+        for (int j = 0; j < first_own; ++j) {
+          const int slot = (g + j) & 3;
+          if (!begin()) break;
           const int key0 = (c.k0 + j) * 128;
           float alpha = 1.f;  // what l and O are to be multiplied by
-          float beta = 1.f;   // and O besides, for its unit
-          if (__builtin_expect(chunk_own(c.k0 + j, rq.len, sure), 0)) {
-            const OwnTile own = chunk_own_tile(s_addr, cs.own_up[slot][0], cs.absent[slot], factor,
-                                               lim - key0, m, v_up == 0.f ? 0x1p-126f : v_up);
-            m = own.m;
-            v_up = own.v_up;
-            alpha = own.alpha;
-            beta = own.beta;
-            l = fmaf(l, alpha, own.sum);
-          } else {
 #pragma unroll
           for (int w = 0; w < 4; ++w) v_size = max(v_size, cs.size[slot][w][1]);
           const float next_up = chunk_up(chunk_size(v_size)) * 0x1p-32f;
-          if (next_up != v_up) {
-            beta = v_up / next_up;
-            v_up = next_up;
-          }
           // (not 0: a hidden key's score is minus infinity times it; scores in these
           // units stay below 2^31)
           const float f = fmaxf(factor * cs.k_up[slot], 1e-30f);
@@ -729,25 +759,16 @@ __global__ void __launch_bounds__(kChunkWarps * 32, 1)
             tmem_st_32x32b_x16(s_addr + 16 * q, pk);
           }
           l = fmaf(l, alpha, sum.x + sum.y);
-          }
-          // ---- O follows the reference and its unit
-          alpha *= beta;
-          if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-            // (S of this tile was issued after the last P V, which is done)
-#pragma unroll 1
-            for (int q = 0; q < D / 32; ++q) {
-              uint32_t oc[32];
-              tmem_ld_32x32b_x32(o_addr + 32 * q, oc);
-              tmem_wait_ld_regs(oc);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) oc[i] = __float_as_uint(__uint_as_float(oc[i]) * alpha);
-              tmem_st_32x32b_x32(o_addr + 32 * q, oc);
-            }
-          }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(L::kPFull + t));
+          end(j, alpha, next_up);
+        }
+        for (int j = first_own; j < n && ok; ++j) {
+          const int slot = (g + j) & 3;
+          if (!begin()) break;
+          const OwnTile own = chunk_own_tile(s_addr, cs.own_up[slot][0], cs.absent[slot], factor,
+                                             lim - (c.k0 + j) * 128, m, v_up == 0.f ? 0x1p-126f : v_up);
+          m = own.m;
+          l = fmaf(l, own.alpha, own.sum);
+          end(j, own.alpha, own.v_up);
         }
         if (!ok) break;
         g += c.most;
