@@ -168,9 +168,9 @@ __device__ __forceinline__ float kv4_scale(float span) {
 // A group with an infinity, a NaN or a span beyond the largest float reads back
 // as NaN.
 //
-// Bound by instructions as much as by memory: about 8 an element besides the
-// reduction.  16384 tokens of 8 heads, d = 128 (86 MB): 29.7 us with cold caches,
-// 2.9 TB/s, issue slots 70 % taken; 32 tokens and their gather 4.2 us.
+// Bound by instructions as much as by memory: 17 an element with the reduction and
+// the walk.  16384 tokens of 8 heads, d = 128 (86 MB): 28.1 us with cold caches,
+// 3.1 TB/s, issue slots 68 % taken; 32 tokens and their gather 4.7 us.
 template <int D>
 __device__ __forceinline__ void append_words(const Kv4StoreParams& p, const StoreWords<D>& w,
                                              long long tile, int row, const uint32_t (&r)[8]) {
@@ -284,8 +284,9 @@ __global__ void __launch_bounds__(kStoreThreads) kv4_append_kernel(const __grid_
 // Reads slots back: lowest + scale n, one fused multiply-add (scale n has 12
 // bits, so only its sum is rounded) and one rounding to bf16.  Slots outside
 // the cache give zeros.
-// Bound by latency and instructions (issue slots 54 % taken): the same 16384
-// tokens (86 MB) 21.8 us with cold caches, 4.0 TB/s; both together 46.4 us.
+// Two tokens of three loads in flight a thread, 10 instructions an element (issue
+// slots 55 % taken): the same 16384 tokens (86 MB) 21.4 us with cold caches,
+// 4.0 TB/s; both together 47.4 us.
 template <int D>
 __global__ void __launch_bounds__(kStoreThreads) kv4_gather_kernel(const __grid_constant__ Kv4StoreParams p) {
   using L = Kv4Tile<D>;
@@ -403,7 +404,7 @@ __device__ __forceinline__ int plan_find(const int* cu, int n, int x) {
 // range (which may be updated in place) are written after a cluster barrier.
 //
 // Bound by latency: the loads of lengths, the scan, and the loads of pages.
-// 8 requests 4.8 us, 1023 requests with 64 prompts (0.46 MB) 11.7 us.
+// 8 requests 5.0 us, 1023 requests with 64 prompts (0.46 MB) 11.9 us.
 __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const __grid_constant__ Kv4PlanParams p) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();

@@ -29,16 +29,19 @@
 // 2^14) and write O.
 //
 // Bound: the tensor cores, the softmax and putting K and V together share the
-// SM about evenly, and a row's softmax (3.7 k cycles a 128-key tile) with the two
-// MMAs that follow it (1 k) makes the chain that sets the pace: the MMA warp
-// waits for P 1.7 k of 5.6 k cycles a tile.  The codes are read once an item, a
+// SM about evenly (issue slots 52 % taken, the tensor pipe 39 %), and a row's
+// softmax with the two MMAs that follow it makes the chain that sets the pace (by
+// clock stamps, in the form of 598 us below: 3.7 k and 1 k cycles, the MMA warp
+// waiting for P 1.7 k of 5.6 k a 128-key tile).  The codes are read once an item, a
 // quarter of the bytes of a bf16 cache.  Two requests of 1000 queries, on 16384
-// and 3000 keys, H=32/8 d=128 (301 GFLOP): 368 us, 818 TFLOP/s; two of 1024 on
-// 16384 (533 GFLOP) 598 us, 891.  Kept steps, whole calls of the first:
+// and 3000 keys, H=32/8 d=128 (301 GFLOP): 398 us, 756 TFLOP/s; two of 1024 on
+// 16384 (533 GFLOP) 635 us, 839.  Kept steps, whole calls of the first:
 // probabilities of a whole row held in registers 929 us; 32 columns at a time
 // 492; K and V by a group of four warps each 450 (as two copies of the code 597:
 // the instruction cache); one copy of the column code 442; the join told what to
-// do 435; a job's fixed cost counted as work 388; no spills in the MMA warp 368.
+// do 435; a job's fixed cost counted as work 388; no spills in the MMA warp 368
+// (the second 598); codes as normal numbers and own units, for the precision above,
+// 405 (646), the latter out of the way of the ordinary tiles 398 (635).
 #pragma once
 
 #include "kv4_attend.cuh"

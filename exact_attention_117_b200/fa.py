@@ -3,8 +3,9 @@
 Every step of the computation runs in the CUDA library ``libfa_b200.so``; this
 module only checks tensor properties, takes device pointers and the current
 stream from torch, and turns status codes into exceptions (through ctypes, the
-rotary and 4-bit cache calls through the extension module of csrc/binding.cpp).  There is no fallback: if the library is missing or not built for
-this GPU, every call raises.
+rotary and 4-bit cache calls through the extension module of csrc/binding.cpp).
+There is no fallback: if the library is missing or not built for this GPU, every
+call raises.
 """
 from __future__ import annotations
 
@@ -313,8 +314,9 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, factor: float = 1
     ``factor`` above 1 positions are interpolated: by ``factor`` in every pair
     or, given the ``original_length``, only in the pairs that turn fewer than
     ``slow_turns`` times in it, not at all in those that turn more than
-    ``fast_turns`` times, in proportion between; the amplitude is then
-    ``0.1 ln(factor) + 1``."""
+    ``fast_turns`` times, in proportion to their turns between; the amplitude is
+    then ``0.1 ln(factor) + 1``.  (A model whose ramp runs over the pairs' index, the
+    logarithm of the turns, has other frequencies between: pass its own.)"""
     if rotary_dim < 2 or rotary_dim % 2:
         raise ValueError("rotary_dim must be even and positive")
     if not (factor >= 1.0 and base > 0.0 and fast_turns > slow_turns):
@@ -338,7 +340,8 @@ def rotary(q, k, positions, inv_freq, interleaved: bool = False, amplitude: floa
     packed ``[tokens, heads, d]`` goes in as ``x.transpose(0, 1)[None]``.
     ``positions``: int32 or int64 ``[N]`` or ``[B, N]``.  The first
     ``2 * len(inv_freq)`` channels turn, in pairs ``(i, i + len(inv_freq))`` or,
-    ``interleaved``, ``(2i, 2i + 1)``.  Outputs may be the inputs."""
+    ``interleaved``, ``(2i, 2i + 1)``.  Outputs may be the inputs.  Like every call
+    here it records nothing for autograd: the gradient is :func:`rotary_backward`."""
     st, out_q, out_k = (_native or _load_native()).rotary(
         q, k, positions, inv_freq, interleaved, amplitude, out_q, out_k, _stream_arg(stream), False)
     if st:
@@ -381,7 +384,8 @@ def kv4_plan(lengths, new_lengths, block_table, free_pages, free_range, page_siz
     ``lengths`` (int32 ``[requests]``) to ``new_lengths``.  ``block_table``
     (int32 ``[requests, width]``) and ``free_pages`` (int32 ring, live from
     ``free_range[0]`` to ``free_range[1]``, int64) are updated in place;
-    lengths and range too if they are passed as their own outputs.  See
+    lengths and range too if they are passed as their own outputs.  The tensors that
+    the call makes share one allocation, which lives as long as any of them.  See
     ``fa_kv4_plan`` in include/fa.h for the statuses."""
     st, *out = (_native or _load_native()).plan(
         lengths, new_lengths, block_table, free_pages, free_range, page_size, max_tokens,
@@ -424,7 +428,9 @@ def kv4_attention(q, cache, block_table, lengths, cu_tokens, max_tokens: int,
     and the newest of its ``lengths[b]`` (int32) cached tokens; ``block_table``
     (int32 ``[requests, width]``) lists its pages.  ``max_tokens``: an upper
     bound on a request's query rows (it chooses the kernel).  Rows that see no
-    key get zeros and -inf; rows of no request are left as they are."""
+    key get zeros and -inf; rows of no request are left as they are.  What tokens
+    hold that a row does not see changes none of its bits; the precision is
+    ``fa_kv4_attention``'s in include/fa.h."""
     st, out, lse = (_native or _load_native()).attention(
         q, cache, block_table, lengths, cu_tokens, max_tokens, causal, scale, out, lse, workspace,
         _stream_arg(stream))
