@@ -404,11 +404,12 @@ struct Kv4State {
   float lo_sum[NT][D / 64][2];  // sum of P times V's lowest values
   float l[NT][2], m[NT][2];
   uint32_t w[NT];  // byte 2 group + r: the unit w = 2^(2 byte - 127) of P s 2^-10; byte 0: w = 0
+  float w_most[D / 64];  // the largest w of the lane's rows times 2^-4
 };
 __device__ __forceinline__ float kv4_unit(uint32_t w, int gp, int r) {
   return __uint_as_float(__byte_perm(w, 0, 0x444 | (2 * gp + r) << 12));
 }
-// The unit that brings `big` to [8, 32), and the least that a unit was found for.
+// The unit that brings `big` to [8, 32).
 __device__ __forceinline__ uint32_t kv4_unit_byte(float big) {
   return min(max((258 - static_cast<int>(__float_as_uint(big) >> 23)) >> 1, 2), 126);
 }
@@ -417,6 +418,7 @@ __device__ __forceinline__ float kv4_unit_ratio(uint32_t to, uint32_t from) {
   const int steps = static_cast<int>(to) - static_cast<int>(from);
   return from == 0 || steps < -63 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + 2 * min(steps, 63)) << 23);
 }
+// The least of the row's largest P s for which a unit may stand.
 __device__ __forceinline__ float kv4_unit_least(float unit) {
   return unit == 0.f ? 0.f : __uint_as_float(0x80800000u - __float_as_uint(unit));  // 8 / unit
 }
@@ -489,9 +491,9 @@ __device__ __forceinline__ void kv4_tiles(const uint8_t* tile, const Kv4Lane<D>&
   auto odd = [&](int u) { return kTiles == 2 ? u == 1 : ((key0 >> 4) & 1) != 0; };
   int key[kTok];
   float vs[kTok][kGroups], vl[kTok][kGroups], x[NT][2 * kTok], y[NT][2 * kTok];
-  float most = 0.f;
-  // (s times 2^-10, so that its product with P below 2^8 is finite for every s;
-  // negative for the tiles taken from above)
+  float most = 0.f, large = 0.f;
+  // (s times 2^-10, so that its product with P is finite for every s; negative for
+  // the tiles taken from above)
 #pragma unroll
   for (int i = 0; i < kTok; ++i) {
     key[i] = key0 + kv4_tau(lane >> 2) + 8 * i;
@@ -502,6 +504,13 @@ __device__ __forceinline__ void kv4_tiles(const uint8_t* tile, const Kv4Lane<D>&
       vs[i][gp] = gone ? 0.f : s_v * (odd(i >> 1) ? -0x1p-10f : 0x1p-10f);
       vl[i][gp] = gone ? 0.f : odd(i >> 1) ? fmaf(15.f, s_v, lowest) : lowest;
     }
+  }
+#pragma unroll
+  for (int gp = 0; gp < kGroups; ++gp) {
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < kTok; i += 2) top = fmax3(fabsf(vs[i][gp]), fabsf(vs[i + 1][gp]), top);
+    large = fmaxf(large, top * st.w_most[gp]);
   }
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -521,11 +530,28 @@ __device__ __forceinline__ void kv4_tiles(const uint8_t* tile, const Kv4Lane<D>&
 #pragma unroll
     for (int c = 0; c < 2 * kTok; c += 2) most = fmax3(y[nt][c], y[nt][c + 1], most);
   }
-  // ---- a row's running reference moves only when one of its scores passes it by
-  // 2^8: most tiles need no reduction over lanes
-  const bool moves = __any_sync(0xffffffffu, most > 8.f);
-  float fall[NT][2];  // what P of the keys so far is multiplied by
-  if (moves) {
+  // ---- A row's reference moves only when one of its scores passes it by 2^8, its
+  // groups' units with it, and where a P s would pass 2^15 (fp16 ends below 2^16):
+  // most tiles need no reduction over lanes.  P is below 2^8, so only a tile with a
+  // scale of V beyond 2^7 in some row's unit has its products looked at.  (What
+  // follows is seldom run and long: fetched anew it costs some 30000 cycles, so that
+  // 2^4 in place of 2^8 made 8 drafted tokens of 4 heads twice as slow.)
+  bool over = most > 8.f;
+  if (__any_sync(0xffffffffu, fmaxf(most, large) > 8.f)) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int gp = 0; gp < kGroups; ++gp)
+#pragma unroll
+        for (int c = 0; c < 2 * kTok; ++c)
+          over |= ex2_approx(y[nt][c]) * fabsf(vs[c >> 1][gp]) * kv4_unit(st.w[nt], gp, c & 1) > 32768.f;
+    over = __any_sync(0xffffffffu, over);
+  } else {
+    over = false;
+  }
+  if (over) {
+#pragma unroll
+    for (int gp = 0; gp < kGroups; ++gp) st.w_most[gp] = 0.f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -536,24 +562,45 @@ __device__ __forceinline__ void kv4_tiles(const uint8_t* tile, const Kv4Lane<D>&
           if (!kMasked || key[c >> 1] < lim[nt][r]) hi = fmaxf(hi, x[nt][c]);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        const bool over = hi - st.m[nt][r] > 8.f;
-        const float f = over ? ex2_approx(st.m[nt][r] - hi) : 1.f;
-        st.m[nt][r] = over ? hi : st.m[nt][r];
-        fall[nt][r] = f;
+        const bool moves = hi - st.m[nt][r] > 8.f;
+        const float f = moves ? ex2_approx(st.m[nt][r] - hi) : 1.f;
+        st.m[nt][r] = moves ? hi : st.m[nt][r];
         st.l[nt][r] *= f;
-#pragma unroll
-        for (int gp = 0; gp < kGroups; ++gp) st.lo_sum[nt][gp][r] *= f;
-#pragma unroll
-        for (int j = 0; j < kVW; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            st.acc[j][i][nt][r] *= f;
-            st.acc[j][i][nt][r + 2] *= f;
-          }
 #pragma unroll
         for (int c = r; c < 2 * kTok; c += 2) {
           y[nt][c] = __fsub_rn(x[nt][c], st.m[nt][r]);
           if (kMasked && key[c >> 1] >= lim[nt][r]) y[nt][c] = -INFINITY;
+        }
+        float weight[kGroups] = {};  // the largest P s of the tile
+#pragma unroll
+        for (int gp = 0; gp < kGroups; ++gp) {
+#pragma unroll
+          for (int c = r; c < 2 * kTok; c += 2)
+            if (!kMasked || key[c >> 1] < lim[nt][r])
+              weight[gp] = fmaxf(weight[gp], ex2_approx(y[nt][c]) * fabsf(vs[c >> 1][gp]));
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1)
+            weight[gp] = fmaxf(weight[gp], __shfl_xor_sync(0xffffffffu, weight[gp], o));
+        }
+#pragma unroll
+        for (int gp = 0; gp < kGroups; ++gp) {
+          st.lo_sum[nt][gp][r] *= f;
+          const int at = 8 * (2 * gp + r);
+          const uint32_t from = st.w[nt] >> at & 0xffu;
+          const float old = kv4_unit(st.w[nt], gp, r);
+          uint32_t to = from;
+          float fall = f;
+          if (moves || weight[gp] * old > 32768.f) {
+            to = kv4_unit_byte(fmaxf(kv4_unit_least(old) * f, weight[gp]));
+            fall *= kv4_unit_ratio(to, from);
+          }
+          st.w[nt] = (st.w[nt] & ~(0xffu << at)) | to << at;
+          st.w_most[gp] = fmaxf(st.w_most[gp], kv4_unit(st.w[nt], gp, r) * 0x1p-4f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            st.acc[gp][i][nt][r] *= fall;
+            st.acc[gp][i][nt][r + 2] *= fall;
+          }
         }
       }
   }
@@ -567,59 +614,22 @@ __device__ __forceinline__ void kv4_tiles(const uint8_t* tile, const Kv4Lane<D>&
       e[c] = ex2_approx(y[nt][c]);
       st.l[nt][c & 1] += e[c];
     }
-    // The fragments of P s, a second time where a group's unit moves: with its row's
-    // reference, and where a P s would pass 2^15 (fp16 ends below 2^16).
-#pragma unroll 1
-    for (int pass = 0;; ++pass) {
-      float top = 0.f;
 #pragma unroll
-      for (int gp = 0; gp < kGroups; ++gp) {
-        const float2 unit = make_float2(kv4_unit(st.w[nt], gp, 0), kv4_unit(st.w[nt], gp, 1));
+    for (int gp = 0; gp < kGroups; ++gp) {
+      const float2 unit = make_float2(kv4_unit(st.w[nt], gp, 0), kv4_unit(st.w[nt], gp, 1));
 #pragma unroll
-        for (int i = 0; i < kTok; ++i) {
-          float2 v = mul_f32x2(make_float2(e[2 * i] * vs[i][gp], e[2 * i + 1] * vs[i][gp]), unit);
-          if (kMasked && key[i] >= lim[nt][0]) v.x = 0.f;
-          if (kMasked && key[i] >= lim[nt][1]) v.y = 0.f;
-          top = fmax3(fabsf(v.x), fabsf(v.y), top);
-          pb[i >> 1][nt][gp][i & 1] = transpose8(pack_f16x2(v.x, v.y));
-        }
-      }
-      if (pass == 1 || !__any_sync(0xffffffffu, moves || top > 32768.f)) break;
-      uint32_t next = st.w[nt];
-#pragma unroll
-      for (int gp = 0; gp < kGroups; ++gp)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float hi = 0.f;
-#pragma unroll
-          for (int c = r; c < 2 * kTok; c += 2)
-            if (!kMasked || key[c >> 1] < lim[nt][r]) hi = fmaxf(hi, fabsf(e[c] * vs[c >> 1][gp]));
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-          const float old = kv4_unit(st.w[nt], gp, r), was = moves ? fall[nt][r] : 1.f;
-          if (was == 1.f && !(hi * old > 32768.f)) continue;
-          const uint32_t byte = kv4_unit_byte(fmaxf(kv4_unit_least(old) * was, hi));
-          const int at = 8 * (2 * gp + r);
-          const float f = kv4_unit_ratio(byte, st.w[nt] >> at & 0xffu);
-          next = (next & ~(0xffu << at)) | byte << at;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            st.acc[gp][i][nt][r] *= f;
-            st.acc[gp][i][nt][r + 2] *= f;
-          }
-        }
-      st.w[nt] = next;
-    }
-#pragma unroll
-    for (int gp = 0; gp < kGroups; ++gp)
-#pragma unroll
-      for (int i = 0; i < kTok; ++i)
+      for (int i = 0; i < kTok; ++i) {
+        float2 v = mul_f32x2(make_float2(e[2 * i] * vs[i][gp], e[2 * i + 1] * vs[i][gp]), unit);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const bool hidden = kMasked && key[i] >= lim[nt][r];
+          if (hidden) (r ? v.y : v.x) = 0.f;
           st.lo_sum[nt][gp][r] = hidden ? st.lo_sum[nt][gp][r]
                                         : fmaf(e[2 * i + r], vl[i][gp], st.lo_sum[nt][gp][r]);
         }
+        pb[i >> 1][nt][gp][i & 1] = transpose8(pack_f16x2(v.x, v.y));
+      }
+    }
   }
   // ---- O^T += V^T P^T
 #pragma unroll
