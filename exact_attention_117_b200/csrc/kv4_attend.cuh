@@ -22,15 +22,16 @@
 // and channels on the 16-row side of m16n8k16, so a single token of a group of
 // up to 8 heads wastes little.
 //
-// Bound: at long contexts the memory, as far as the instructions let it (266 a
-// 16-key tile of d = 128, issue slots 55 % taken): 3 requests of 100000 to 131072
-// keys, H=32/8 d=128, 89 us, 4.4 TB/s (twice the keys take longer by 5.4 TB/s);
-// 64 requests of 200 to 8192 keys 77 us, 4.1 TB/s, the rest being what a job and
+// Bound: at long contexts the memory, as far as the instructions let it (261 a
+// 16-key tile of d = 128, issue slots 56 % taken): 3 requests of 100000 to 131072
+// keys, H=32/8 d=128, 88 us, 4.4 TB/s (more keys take longer by 5.6 TB/s);
+// 64 requests of 200 to 8192 keys 76 us, 4.1 TB/s, the rest being what a job and
 // the join of its pieces cost; with more row tiles the latency of a tile, as few
-// warps fit: 32 requests of 4096 keys with 5 drafted tokens 86 us (151 MB), 24 of
-// up to 4096 with 5, H=16/4 d=64, 24 us; one request of 1000 keys 9.0 us, two
-// launches and the latency of one tile.  The units of P s a row and group cost 2 %
-// of a decode step and 5 to 13 % with 2 to 4 row tiles, against one unit a warp.
+// warps fit: 32 requests of 4096 keys with 5 drafted tokens 80 us (151 MB), 24 of
+// up to 4096 with 5, H=16/4 d=64, 23.6 us; one request of 1000 keys 9.1 us, two
+// launches and the latency of one tile.  The units of P s a row and group cost
+// nothing that shows with one row tile, 2 to 4 % with two and three, 13 % with four
+// (spilled registers), against one unit a warp.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -35,13 +35,13 @@
 // waiting for P 1.7 k of 5.6 k a 128-key tile).  The codes are read once an item, a
 // quarter of the bytes of a bf16 cache.  Two requests of 1000 queries, on 16384
 // and 3000 keys, H=32/8 d=128 (301 GFLOP): 398 us, 756 TFLOP/s; two of 1024 on
-// 16384 (533 GFLOP) 635 us, 839.  Kept steps, whole calls of the first:
+// 16384 (533 GFLOP) 637 us, 837.  Kept steps, whole calls of the first:
 // probabilities of a whole row held in registers 929 us; 32 columns at a time
 // 492; K and V by a group of four warps each 450 (as two copies of the code 597:
 // the instruction cache); one copy of the column code 442; the join told what to
 // do 435; a job's fixed cost counted as work 388; no spills in the MMA warp 368
 // (the second 598); codes as normal numbers and own units, for the precision above,
-// 405 (646), the latter out of the way of the ordinary tiles 398 (635).
+// 405 (646), the latter out of the way of the ordinary tiles 398 (637).
 #pragma once
 
 #include "kv4_attend.cuh"
@@ -186,8 +186,12 @@ struct ChunkShared {
 // the unit times 2^-32 are normal numbers: values below 2^-86 count as small
 // parts of 2^-86.
 __device__ __forceinline__ int chunk_size(int exponent) { return min(max(exponent, 41), 254); }
-__device__ __forceinline__ float chunk_up(int size) { return __uint_as_float(static_cast<uint32_t>(size - 8) << 23); }
-__device__ __forceinline__ float chunk_down(int size) { return __uint_as_float(static_cast<uint32_t>(262 - size) << 23); }
+__device__ __forceinline__ float chunk_up(int size) {
+  return __uint_as_float(static_cast<uint32_t>(size - 8) << 23);
+}
+__device__ __forceinline__ float chunk_down(int size) {
+  return __uint_as_float(static_cast<uint32_t>(262 - size) << 23);
+}
 // Whether key tile `tile` has own units: some row of the item does not see all
 // of its keys (`sure`: what the first row sees).
 __device__ __forceinline__ bool chunk_own(int tile, int len, int sure) { return min(128 * tile + 128, len) > sure; }

@@ -105,11 +105,11 @@ fa_status store_params(fa::Kv4StoreParams* p, const void* k, const void* v, cons
 // The kernel for `max_tokens` queries a request: 1 to 4 row tiles of 8 on mma
 // (kv4_attend.cuh), 0: 256 rows on tcgen05 (kv4_chunk.cuh), whose time hardly
 // depends on the rows below 128.  us on one B200, mma / tcgen05, 16 requests of
-// 4096 keys: d = 128, 8 heads, 32 rows 68 / 95, 48 rows 110 / 95, 64 rows 112 / 95,
-// 128 rows 201 / 96; d = 64, 16 heads on 4, 64 rows 45 / 48, 96 rows 57 / 48, 128
-// rows 71 / 49; 4 requests of 32768 keys cross at the same rows.  (One request
+// 4096 keys: d = 128, 8 heads, 32 rows 68 / 95, 48 rows 109 / 95, 64 rows 112 / 95,
+// 128 rows 197 / 96; d = 64, 16 heads on 4, 64 rows 44 / 48, 96 rows 55 / 49, 128
+// rows 69 / 49; 4 requests of 32768 keys cross at the same rows.  (One request
 // of 4096 keys leaves most of the GPU idle either way, and mma is ahead up to 128
-// rows, 33 / 35 us.)  The longest request chooses for the whole call: single tokens
+// rows, 35 / 35 us.)  The longest request chooses for the whole call: single tokens
 // beside a prompt go with it.
 int attend_kind(int max_tokens, int group, int d) {
   const long long rows = static_cast<long long>(max_tokens) * group;
@@ -136,11 +136,11 @@ fa_status launch_join(void (*kernel)(fa::Kv4AttendParams, int), int ctas, int ro
 
 // Leading units of a job (kv4_attend.cuh): two, about what a job costs besides its
 // keys.  us without / with them on one B200, d = 128, H=32/8: 64 requests of 200 to
-// 8192 keys 88 / 77, 256 of 100 to 2000 120 / 97, 16 of 100 to 8000 33 / 26.5,
-// 64 of 4096 72 / 73; chunks: 1000 queries on 16384 keys and on 3000 454 / 398, one
+// 8192 keys 86 / 76, 256 of 100 to 2000 118 / 95, 16 of 100 to 8000 33 / 26,
+// 64 of 4096 71 / 71; chunks: 1000 queries on 16384 keys and on 3000 454 / 398, one
 // of 1000 queries on 1000 keys 59 / 47.  With fewer jobs than CTAs one is enough, and
 // where they are far fewer hardly a CTA has more than one job to begin, and leading
-// units only take CTAs from the keys (one request of 4096 keys 13.3 / 13.7).
+// units only take CTAs from the keys (one request of 4096 keys 13.4 / 13.8).
 int attend_lead(const fa::Kv4AttendParams& p, int rows, int ctas, bool chunk) {
   const long long each = (static_cast<long long>(p.tokens) * p.group + p.requests - 1) / p.requests;
   const long long jobs = (each + rows - 1) / rows * p.requests * p.kv_heads;
